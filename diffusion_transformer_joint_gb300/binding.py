@@ -31,7 +31,8 @@ EXPORTS = ("flux_rope_tables", "flux_rope_tables_packed", "flux_joint_rope_atten
            "flux_joint_rope_attention_extract_workspace", "flux_joint_rope_attention_extract",
            "flux_joint_rope_attention_cached_workspace", "flux_joint_rope_attention_cached",
            "flux_joint_qknorm_rope_attention_extract", "flux_joint_qknorm_rope_attention_cached",
-           "flux_qkv_mlp_proj", "flux_query_status", "flux_status_string")
+           "flux_qkv_mlp_proj", "flux_linear", "flux_modulated_norm", "flux_query_status",
+           "flux_status_string")
 
 
 class FluxError(RuntimeError):
@@ -119,6 +120,13 @@ def load(path: str | None = None):
             lib.flux_joint_qknorm_rope_attention_cached.restype = I32
             lib.flux_qkv_mlp_proj.argtypes = [V, V, I64, I32, I32, I32, I64, V, V, V, V, V, V]
             lib.flux_qkv_mlp_proj.restype = I32
+            lib.flux_linear.argtypes = [V, I64, I64, I32, V, I64, I64, I32, V, I64, I32, I64, I64,
+                                        I32, V, V, I64, I32, V, I64, I64, V, I64, I64, V, V]
+            lib.flux_linear.restype = I32
+            lib.flux_modulated_norm.argtypes = [V, I64, I64, I32, V, I64, I64, V, I64, V, I64, V,
+                                                I64, I32, I32, I64, I32, I32, F, V, I64, I64, V,
+                                                I64, I64, V]
+            lib.flux_modulated_norm.restype = I32
             lib.flux_query_status.argtypes = [V, V]
             lib.flux_query_status.restype = I32
             lib.flux_status_string.argtypes = [I32]
@@ -615,6 +623,178 @@ def qkv_mlp_proj(x, w, H, mlp=None, q=None, k=None, v=None, act=None, status=Non
     if rc != 0:
         raise FluxError("flux_qkv_mlp_proj", rc, lib)
     return q, k, v, act
+
+
+ACTIVATIONS = {None: 0, "silu": 1, "gelu_tanh": 2, "swiglu": 3}
+NORMS = {"layer": 0, "rms": 1}
+
+
+def _token_rows(name, t, shape, dtype, device):
+    """(address, batch stride, token stride) of a tensor of token rows, [B, S,
+    width] or [S, width] with contiguous channels; raises for anything else."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name} must have contiguous channels, got strides {st}")
+    return t.data_ptr(), (st[0] if len(st) == 3 else 0), st[-2]
+
+
+def _vector(name, t, B, width, dtype, device):
+    """(address, batch stride) of a vector [width], or of one per batch element
+    [B, width] (a stride of 0 where all are the same)."""
+    if t.shape[-1:] != (width,) or t.dim() > 2 or (t.dim() == 2 and t.shape[0] not in (1, B)):
+        raise ValueError(f"{name} must be [{width}] or [{B}, {width}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    st = t.stride()
+    if width > 1 and st[-1] != 1:
+        raise ValueError(f"{name} must be contiguous, got strides {st}")
+    return t.data_ptr(), (st[0] if t.dim() == 2 and t.shape[0] == B and B > 1 else 0)
+
+
+def _vector_type(names, vecs):
+    """The one type of the vectors given: (dtype, vec_f32)."""
+    import torch
+
+    dtype = None
+    for name, t in zip(names, vecs):
+        if t is None:
+            continue
+        if t.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError(f"{', '.join(names)} must have one type")
+        dtype = t.dtype
+    return dtype, int(dtype == torch.float32)
+
+
+def _stream_of(x, stream):
+    """(the stream, its handle) for a call on x's device, which must be current."""
+    import torch
+
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor (no CPU path exists)")
+    cur = torch.cuda.current_stream()
+    if x.device.index != cur.device_index:
+        raise ValueError(f"x is on {x.device}, the current device is {cur.device}")
+    if stream is None:
+        stream = cur
+    elif stream.device_index != cur.device_index:
+        raise ValueError(f"the stream is on {stream.device}, x on {x.device}")
+    return stream, stream.cuda_stream
+
+
+def linear(x, w, x2=None, bias=None, act=None, gate=None, residual=None, out=None, status=None,
+           stream=None):
+    """A linear layer with its epilogue: residual + gate * act([x | x2] W^T + bias).
+
+    x: bf16 CUDA [B, S, K] (or [S, K]); x2 more input channels [B, S, K2]; w
+    bf16 [N, K + K2], or [2 N, K + K2] for act "swiglu" (the gate rows, then the
+    linear rows). act: None, "silu", "gelu_tanh" or "swiglu". bias [N] ([2 N])
+    and gate [N] or [B, N] are both bf16 or both fp32; residual and ``out`` are
+    bf16 [B, S, N] (``out=residual`` updates a stream in place). Token tensors
+    and w may have strides between rows and batch elements (views of a joint
+    sequence, of a wider buffer or of w's columns). ``status`` (int32 [1],
+    cleared here when allocated) receives a device timeout. Returns out.
+    """
+    import torch
+
+    lib = load()
+    stream, handle = _stream_of(x, stream)
+    dev, bf16 = x.device, torch.bfloat16
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [B, S, K] or [S, K], got {tuple(x.shape)}")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {list(ACTIVATIONS)}, got {act!r}")
+    lead = x.shape[:-1]
+    B, S, K = (1, *x.shape) if x.dim() == 2 else x.shape
+    K2 = 0 if x2 is None else int(x2.shape[-1])
+    if w.dim() != 2 or w.shape[1] != K + K2:
+        raise ValueError(f"w must be [rows, {K + K2}], got {tuple(w.shape)}")
+    rows = w.shape[0]
+    if act == "swiglu" and rows % 2:
+        raise ValueError(f"w must have two equal halves of rows, got {rows}")
+    N = rows // 2 if act == "swiglu" else rows
+    shape = (*lead, N)
+    xp, xb, xr = _token_rows("x", x, x.shape, bf16, dev)
+    wp, _, wr = _token_rows("w", w, w.shape, bf16, dev)
+    x2p, x2b, x2r = (_token_rows("x2", x2, (*lead, K2), bf16, dev) if x2 is not None
+                     else (None, 0, 0))
+    rp, rb, rr = (_token_rows("residual", residual, shape, bf16, dev) if residual is not None
+                  else (None, 0, 0))
+    vt, vec_f32 = _vector_type(("bias", "gate"), (bias, gate))
+    bp = _vector("bias", bias, 1, rows, vt, dev)[0] if bias is not None else None
+    gp, gb = _vector("gate", gate, B, N, vt, dev) if gate is not None else (None, 0)
+    if out is None or status is None:
+        with torch.cuda.stream(stream):  # memory of the stream that uses it
+            if out is None:
+                out = torch.empty(shape, dtype=bf16, device=dev)
+            if status is None:
+                status = torch.zeros(1, dtype=torch.int32, device=dev)
+    op, ob, orow = _token_rows("out", out, shape, bf16, dev)
+    if status.dtype != torch.int32 or status.numel() < 1 or status.device != dev:
+        raise ValueError(f"status must hold one int32 on {dev}")
+    rc = lib.flux_linear(xp, xb, xr, K, x2p, x2b, x2r, K2, wp, wr, B, S, N, ACTIVATIONS[act], bp,
+                         gp, gb, vec_f32, rp, rb, rr, op, ob, orow, status.data_ptr(), handle)
+    if rc != 0:
+        raise FluxError("flux_linear", rc, lib)
+    return out
+
+
+def modulated_norm(x, scale=None, shift=None, y=None, gate=None, norm="layer", eps=1e-6, out=None,
+                   x_out=None, stream=None):
+    """The modulated norm with the gated residual in front:
+    x_out = x + gate * y, h = norm(x_out) * (1 + scale) + shift.
+
+    x: bf16 or fp32 CUDA [B, S, dim] (or [S, dim]); y bf16 of the same shape.
+    gate, scale and shift [dim] or [B, dim], all bf16 or all fp32. norm:
+    "layer" or "rms", without learned weights. Token tensors may have strides
+    between rows and batch elements; ``x_out=x`` updates the stream in place.
+    Returns h (bf16, into ``out``), or (h, x_out) when y is given.
+    """
+    import torch
+
+    lib = load()
+    stream, handle = _stream_of(x, stream)
+    dev, bf16 = x.device, torch.bfloat16
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [B, S, dim] or [S, dim], got {tuple(x.shape)}")
+    if x.dtype not in (bf16, torch.float32):
+        raise ValueError(f"x must be bfloat16 or float32, got {x.dtype}")
+    if norm not in NORMS:
+        raise ValueError(f"norm must be one of {list(NORMS)}, got {norm!r}")
+    if y is None and (gate is not None or x_out is not None):
+        raise ValueError("gate and x_out need y")
+    shape = x.shape
+    B, S, dim = (1, *shape) if x.dim() == 2 else shape
+    xp, xb, xr = _token_rows("x", x, shape, x.dtype, dev)
+    vt, vec_f32 = _vector_type(("scale", "shift", "gate"), (scale, shift, gate))
+    sp, sb = _vector("scale", scale, B, dim, vt, dev) if scale is not None else (None, 0)
+    fp, fb = _vector("shift", shift, B, dim, vt, dev) if shift is not None else (None, 0)
+    gp, gb = _vector("gate", gate, B, dim, vt, dev) if gate is not None else (None, 0)
+    if out is None or (y is not None and x_out is None):
+        with torch.cuda.stream(stream):  # memory of the stream that uses it
+            if out is None:
+                out = torch.empty(shape, dtype=bf16, device=dev)
+            if y is not None and x_out is None:
+                x_out = torch.empty(shape, dtype=x.dtype, device=dev)
+    hp, hb, hr = _token_rows("out", out, shape, bf16, dev)
+    yp, yb, yr = _token_rows("y", y, shape, bf16, dev) if y is not None else (None, 0, 0)
+    op, ob, orow = (_token_rows("x_out", x_out, shape, x.dtype, dev) if y is not None
+                    else (None, 0, 0))
+    rc = lib.flux_modulated_norm(xp, xb, xr, int(x.dtype == torch.float32), yp, yb, yr, gp, gb, sp,
+                                 sb, fp, fb, vec_f32, B, S, dim, NORMS[norm], float(eps), op, ob,
+                                 orow, hp, hb, hr, handle)
+    if rc != 0:
+        raise FluxError("flux_modulated_norm", rc, lib)
+    return out if y is None else (out, x_out)
 
 
 def query_status(workspace, stream=None) -> int:

@@ -137,6 +137,42 @@ cudaError_t launch_qkv_mlp_proj(const void *x, const void *w, int64_t M, int dim
                                 int64_t mlp, void *q, void *k, void *v, void *act, int *status,
                                 cudaStream_t stream);
 
+// out = residual + gate * act([x | x2] W^T + bias) over tokens [B, S]. Strides
+// are in elements: _bs between batch elements, _rs between token rows (w_rs
+// between W's rows), every one a multiple of 8. K, K2, N multiples of 8.
+struct LinearProblem {
+  const void *x, *x2, *w, *residual;
+  void *out;
+  int64_t x_bs, x_rs, x2_bs, x2_rs, w_rs, r_bs, r_rs, o_bs, o_rs;
+  int64_t B, S, N;
+  int K, K2;
+};
+struct LinearEpilogue;
+
+// The two kernels behind flux_linear (act: a flux_activation). _pair is for
+// any number of rows; _rows takes B * roundup(S, 8) <= kLinearRowsMax.
+constexpr int kLinearRowsMax = 256;
+cudaError_t launch_linear_pair(const LinearProblem &q, const LinearEpilogue &epi, int act,
+                               int *status, cudaStream_t stream);
+cudaError_t launch_linear_rows(const LinearProblem &q, const LinearEpilogue &epi, int act,
+                               int *status, cudaStream_t stream);
+
+// x_out = x + gate * y, h = norm(x_out) * (1 + scale) + shift over tokens
+// [B, S] of `dim` channels. x and x_out are bf16, or fp32 with stream_f32; y
+// and h bf16; gate, scale and shift bf16, or fp32 with vec_f32. y NULL: no
+// residual (x_out and gate unused); scale, shift and gate may be NULL.
+// Strides in elements, multiples of 8 (the vectors' may be 0).
+struct ModulatedNorm {
+  const void *x, *y, *gate, *scale, *shift;
+  void *x_out, *h;
+  int64_t x_bs, x_rs, y_bs, y_rs, gate_bs, scale_bs, shift_bs, xo_bs, xo_rs, h_bs, h_rs;
+  int64_t B, S;
+  int dim, rms, stream_f32, vec_f32;
+  float eps;
+};
+constexpr int kNormMaxDim = 16384;
+cudaError_t launch_modulated_norm(const ModulatedNorm &q, cudaStream_t stream);
+
 // Enqueues the attention kernel. q/k/v/out are [B, S, H, 128] bf16; `table`
 // is the packed table of the joint sequence; status is the device status word.
 // `krot_scratch` (256-byte aligned, krot_scratch_bytes long) lets the CTAs

@@ -1,0 +1,112 @@
+// What the two kernels behind flux_linear share: the problem's description,
+// the activations and the loads of the per-feature vectors.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "flux_attn.h"
+#include "flux_internal.h"
+#include "ptx_sm103a.cuh"
+
+namespace flux {
+
+// The epilogue's operands: out = residual + gate * act(acc + bias). bias,
+// gate and residual may be NULL. Token (b, s) of the launch reads gate row
+// (b * S + s) / gate_rows: a launch may join the batch elements into one run
+// of rows, while the gate still changes every gate_rows of them.
+struct LinearEpilogue {
+  const void *bias, *gate;
+  int64_t gate_bs;    // elements from one gate row to the next
+  int64_t gate_rows;  // rows that share a gate row
+  int vec_f32;        // bias and gate: 1 fp32, 0 bf16
+};
+
+// act(y) in fp32. SiLU y / (1 + e^-y); GELU in its tanh form, of which
+// 0.5 (1 + tanh u) = 1 / (1 + e^-2u) needs one exponential.
+template <int kAct>
+__device__ __forceinline__ float activate(float y) {
+  if constexpr (kAct == FLUX_ACT_SILU) {
+    return y / (1.f + __expf(-y));
+  } else if constexpr (kAct == FLUX_ACT_GELU_TANH) {
+    const float u2 = 1.5957691216057308f * (y + 0.044715f * y * y * y);  // 2 sqrt(2/pi) (...)
+    return y / (1.f + __expf(-u2));
+  } else {
+    return y;
+  }
+}
+
+// Eight consecutive entries of a bf16 or fp32 vector, 16-byte aligned.
+__device__ __forceinline__ void load_vec8(const void *base, int64_t off, int f32, float (&v)[8]) {
+  if (f32) {
+    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off));
+    v[0] = bf16lo_to_f32(w.x), v[1] = bf16hi_to_f32(w.x);
+    v[2] = bf16lo_to_f32(w.y), v[3] = bf16hi_to_f32(w.y);
+    v[4] = bf16lo_to_f32(w.z), v[5] = bf16hi_to_f32(w.z);
+    v[6] = bf16lo_to_f32(w.w), v[7] = bf16hi_to_f32(w.w);
+  }
+}
+
+__device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
+  v[0] = bf16lo_to_f32(w.x), v[1] = bf16hi_to_f32(w.x);
+  v[2] = bf16lo_to_f32(w.y), v[3] = bf16hi_to_f32(w.y);
+  v[4] = bf16lo_to_f32(w.z), v[5] = bf16hi_to_f32(w.z);
+  v[6] = bf16lo_to_f32(w.w), v[7] = bf16hi_to_f32(w.w);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+// Eight features f .. f + 7 of one token through the epilogue, from the
+// accumulators a (and, for SwiGLU, u: the linear half), rounded once to bf16.
+// SwiGLU's bias holds the gate half's N entries, then the linear half's.
+template <int kAct>
+__device__ __forceinline__ uint4 finish8(const LinearEpilogue &e, int64_t N, int64_t f,
+                                         int64_t gate_row, const float (&a)[8],
+                                         const float (&u)[8], bool has_res, uint4 res) {
+  float y[8], b[8] = {};
+  if (e.bias != nullptr) load_vec8(e.bias, f, e.vec_f32, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = a[i] + b[i];
+  if constexpr (kAct == FLUX_ACT_SWIGLU) {
+    float bu[8] = {};
+    if (e.bias != nullptr) load_vec8(e.bias, N + f, e.vec_f32, bu);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = activate<FLUX_ACT_SILU>(y[i]) * (u[i] + bu[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = activate<kAct>(y[i]);
+  }
+  if (e.gate != nullptr) {
+    float g[8];
+    load_vec8(e.gate, gate_row * e.gate_bs + f, e.vec_f32, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] *= g[i];
+  }
+  if (has_res) {
+    float r[8];
+    unpack8(res, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] += r[i];
+  }
+  return pack8(y);
+}
+
+// A 3-D tensor map over bf16 rows [B, S, cols] with the given element
+// strides; one box = box_cols columns x box_rows tokens x box_b batch
+// elements, swizzled over its row (128 bytes for 64 columns, 64 for 32).
+// Elements outside the tensor read as zero and are not written.
+bool make_row_map(CUtensorMap *map, const void *base, int64_t cols, int64_t S, int64_t B,
+                  int64_t row_stride, int64_t batch_stride, uint32_t box_cols, uint32_t box_rows,
+                  uint32_t box_b);
+
+}  // namespace flux

@@ -28,7 +28,9 @@
  * sequence-parallel callers); the reference-image KV
  * modes (extract, cached); and the single-stream block's fused input
  * projection (Q, K, V and the SwiGLU-activated MLP input from one GEMM), the
- * producer of the attention's inputs.
+ * producer of the attention's inputs; and the rest of a block's operators:
+ * the linear layers with bias, activation, gate and residual in the epilogue,
+ * and the modulated norm with the gated residual in front.
  *
  * Conventions shared by every entry point:
  *   - Device pointers refer to memory on the CUDA device that is current on
@@ -385,6 +387,95 @@ int flux_joint_rope_attention_cached(const void *q, const void *k, const void *v
 int flux_qkv_mlp_proj(const void *x, const void *w, int64_t M, int dim, int H, int D,
                       int64_t mlp_hidden, void *q, void *k, void *v, void *act, int32_t *status,
                       void *stream);
+
+/*
+ * The rest of a block ("Diffusers 中 Flux2Transformer2DModel 全面解析", section
+ * 内部架构双流块与单流块: modulation vectors shift, scale and gate per batch
+ * element; a modulated norm before the attention and the feed-forward; their
+ * output products gated onto the residual; one fused output product over
+ * [attention ; MLP] in the single-stream block).
+ *
+ * Strides. These entry points take token rows [B, S, width] whose channels are
+ * contiguous, with a batch stride (_bs) and a token stride (_rs) in elements:
+ * positive multiples of 8, the token stride at least the width (a stride whose
+ * size is 1 is not looked at). So a stream may live inside a joint sequence
+ * or inside the columns of a wider buffer. An output's rows must not share
+ * elements. Token pointers and vectors are 16-byte aligned. Vectors per batch
+ * element (gate, scale, shift) have a batch stride that may be 0 (one vector
+ * for the whole batch), a multiple of 8. vec_f32: the vectors' type, 1 fp32,
+ * 0 bf16.
+ *
+ * Outputs must not overlap inputs or one another (FLUX_ERR_ALIAS), except
+ * that a residual stream may be updated in place: the same pointer and
+ * strides for the residual (x) and the output (x_out). Tensors with the same
+ * strides are compared row by row, others by the address ranges they span.
+ */
+
+typedef enum {
+  FLUX_ACT_NONE = 0,
+  FLUX_ACT_SILU = 1,      /* y / (1 + exp(-y)) */
+  FLUX_ACT_GELU_TANH = 2, /* y/2 (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))) */
+  FLUX_ACT_SWIGLU = 3     /* silu(gate half) * linear half, W has 2 N rows */
+} flux_activation;
+
+typedef enum {
+  FLUX_NORM_LAYER = 0, /* (v - mean v) / sqrt(mean (v - mean v)^2 + eps) */
+  FLUX_NORM_RMS = 1    /* v / sqrt(mean v^2 + eps) */
+} flux_norm;
+
+/*
+ * flux_linear: a linear layer with its epilogue,
+ *   y = [x | x2] W^T + bias  (fp32 accumulation),
+ *   out = residual + gate * act(y), rounded once to bf16 (nearest even).
+ *
+ *   x          device, bf16 [B, S, K]; K a multiple of 8.
+ *   x2, K2     more input channels, bf16 [B, S, K2], after those of x (the
+ *              single-stream block's [attention | MLP] without the
+ *              concatenation); K2 a multiple of 8, 0: none (x2 may be NULL).
+ *   w, w_rs    device, bf16 [N, K + K2] with row stride w_rs (a linear layer's
+ *              weight, or a range of its columns); for FLUX_ACT_SWIGLU
+ *              [2 N, K + K2], the N gate rows, then the N linear rows.
+ *   B, S       1 <= B * S <= 2^30.  N: a multiple of 8, at most 2^28.
+ *   act        a flux_activation.
+ *   bias       [N] ([2 N] for SwiGLU) or NULL.
+ *   gate       [B, N] at batch stride gate_bs, or NULL (1).
+ *   residual   bf16 [B, S, N] or NULL (0); may be `out` itself.
+ *   out        bf16 [B, S, N]; written, not read (unless it is the residual).
+ *   status     device int32 word; the kernel writes FLUX_ERR_DEVICE_TIMEOUT
+ *              there if a bounded wait runs out and never writes it otherwise.
+ * The sums are added in an order that depends on the sizes only: the same call
+ * gives the same bits every time.
+ * Returns FLUX_OK when the kernel was enqueued, else a negative status.
+ */
+int flux_linear(const void *x, int64_t x_bs, int64_t x_rs, int K, const void *x2, int64_t x2_bs,
+                int64_t x2_rs, int K2, const void *w, int64_t w_rs, int B, int64_t S, int64_t N,
+                int act, const void *bias, const void *gate, int64_t gate_bs, int vec_f32,
+                const void *residual, int64_t r_bs, int64_t r_rs, void *out, int64_t o_bs,
+                int64_t o_rs, int32_t *status, void *stream);
+
+/*
+ * flux_modulated_norm: the modulated norm, with the gated residual in front,
+ *   x_out = x + gate * y                       (y NULL: x_out is x),
+ *   h = norm(x_out) * (1 + scale) + shift,
+ * the norm over the dim channels of each token, taken of the fp32 sum before
+ * x_out is rounded to its type.
+ *
+ *   x          device, bf16 [B, S, dim], or fp32 with stream_f32 = 1.
+ *   y, gate    bf16 [B, S, dim] and [B, dim] (gate NULL: 1); y NULL: no
+ *              residual, gate and x_out are not looked at.
+ *   scale, shift  [B, dim] each, or NULL (0).
+ *   dim        a multiple of 8, at most 16384.  1 <= B * S <= 2^30.
+ *   norm       a flux_norm.  eps: finite, >= 0.
+ *   x_out      [B, S, dim] of x's type; may be x itself.
+ *   h          bf16 [B, S, dim].
+ * Returns FLUX_OK when the kernel was enqueued, else a negative status.
+ */
+int flux_modulated_norm(const void *x, int64_t x_bs, int64_t x_rs, int stream_f32, const void *y,
+                        int64_t y_bs, int64_t y_rs, const void *gate, int64_t gate_bs,
+                        const void *scale, int64_t scale_bs, const void *shift, int64_t shift_bs,
+                        int vec_f32, int B, int64_t S, int dim, int norm, float eps, void *x_out,
+                        int64_t xo_bs, int64_t xo_rs, void *h, int64_t h_bs, int64_t h_rs,
+                        void *stream);
 
 /*
  * flux_joint_qknorm_rope_attention_extract / _cached: the two KV modes with

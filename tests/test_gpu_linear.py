@@ -1,0 +1,258 @@
+"""binding.linear against the 64-bit definition: both kernels, every epilogue,
+odd sizes, strided views, one row to offsets past 32 bits."""
+import pytest
+import torch
+
+from diffusion_transformer_joint_gb300 import binding, build
+from tests import block_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    binding.load()
+
+
+def _make(B, S, K, N, K2=0, act=None, bias=False, gate=False, residual=False, vec=torch.bfloat16,
+          seed=0):
+    """CUDA operands drawn on the CPU from one generator."""
+    g = torch.Generator().manual_seed(1000 + seed)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    rows = 2 * N if act == "swiglu" else N
+    ops = dict(x=r(B, S, K).bfloat16(), w=(r(rows, K + K2) * (K + K2) ** -0.5).bfloat16(), act=act)
+    ops["x2"] = r(B, S, K2).bfloat16() if K2 else None
+    ops["bias"] = r(rows).to(vec) if bias else None
+    ops["gate"] = r(B, N).to(vec) if gate else None
+    ops["residual"] = (2 * r(B, S, N)).bfloat16() if residual else None
+    return {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in ops.items()}
+
+
+def _run(ops, **kw):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = binding.linear(status=status, **ops, **kw)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    return out
+
+
+FULL = dict(bias=True, gate=True, residual=True)
+
+
+@pytest.mark.parametrize("B,S,K,N,kw", [
+    (1, 1, 8, 8, {}),                                        # the smallest call
+    (1, 1, 256, 1024, dict(act="silu")),
+    (1, 1, 64, 128, FULL),
+    (2, 1, 512, 384, dict(bias=True)),                       # batch elements joined
+    (1, 2, 72, 40, dict(FULL, act="gelu_tanh")),             # ragged channels and features
+    (1, 8, 200, 136, dict(FULL, act="silu", vec=torch.float32)),
+    (1, 9, 1000, 264, dict(act="swiglu", bias=True)),
+    (3, 5, 136, 72, dict(FULL, act="swiglu")),
+    (1, 16, 4096, 128, dict(bias=True)),                     # channels split over 8 blocks
+    (1, 17, 2048, 248, dict(FULL)),                          # over 8, ragged last feature tile
+    (2, 33, 1096, 328, dict(FULL, K2=520, act="gelu_tanh")),  # the split meets the x | x2 seam
+    (1, 64, 640, 136, dict(K2=8, residual=True)),
+    (1, 77, 768, 520, dict(FULL, act="swiglu", vec=torch.float32)),
+    (4, 64, 320, 192, dict(FULL)),                           # 256 columns
+    (1, 255, 456, 120, dict(K2=72, act="silu", gate=True)),
+    (1, 256, 64, 1032, {}),
+])
+def test_few_rows(B, S, K, N, kw):
+    ops = _make(B, S, K, N, **kw)
+    R.check(_run(ops), R.linear(**ops), f"{B}x{S}x{K}->{N}")
+
+
+@pytest.mark.parametrize("B,S,K,N,kw", [
+    (1, 257, 64, 8, {}),
+    (1, 300, 200, 136, FULL),
+    (1, 512, 128, 256, dict(act="silu", bias=True, vec=torch.float32)),
+    (1, 513, 72, 520, dict(FULL, K2=136, act="gelu_tanh")),
+    (2, 300, 520, 264, dict(FULL, vec=torch.float32)),       # a gate per batch element, joined rows
+    (3, 290, 192, 104, dict(FULL, act="swiglu")),
+    (1, 640, 1032, 72, dict(K2=520, residual=True)),
+    (1, 2500, 96, 744, dict(FULL, act="swiglu", vec=torch.float32)),  # more tiles than pairs
+    (1, 700, 64, 4104, dict(gate=True, residual=True)),
+    (5, 257, 40, 1000, dict(bias=True, act="gelu_tanh")),
+])
+def test_many_rows(B, S, K, N, kw):
+    ops = _make(B, S, K, N, **kw)
+    R.check(_run(ops), R.linear(**ops), f"{B}x{S}x{K}->{N}")
+
+
+@pytest.mark.parametrize("B,S", [(2, 21), (3, 1), (2, 150), (2, 300), (3, 128)])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_views_of_a_joint_sequence(B, S, act):
+    """x, residual and out live in the trailing tokens and a column range of
+    wider buffers; what lies around the output is left as it was."""
+    K, N = 136, 72
+    ops = _make(B, S, K, N, K2=64, act=act, **FULL, seed=S)
+    out_buf = torch.full((B, S + 7, N + 48), 7.0, dtype=torch.bfloat16, device="cuda")
+    for name, width, pad in (("x", K, 16), ("x2", 64, 8), ("residual", N, 24)):
+        buf = torch.full((B, S + 5, width + pad), float("nan"), dtype=torch.bfloat16, device="cuda")
+        buf[:, 5:, 8:8 + width] = ops[name]
+        ops[name] = buf[:, 5:, 8:8 + width]
+    wbuf = torch.full((ops["w"].shape[0], 64 + K + 64 + 8), float("nan"), dtype=torch.bfloat16,
+                      device="cuda")
+    wbuf[:, 64:-8] = ops["w"]
+    ops["w"] = wbuf[:, 64:-8]
+    out = out_buf[:, 7:, 16:16 + N]
+    assert _run(ops, out=out) is out
+    R.check(out, R.linear(**ops), "views")
+    assert bool((out_buf[:, :7] == 7).all())
+    assert bool((out_buf[:, 7:, :16] == 7).all() and (out_buf[:, 7:, 16 + N:] == 7).all())
+
+
+@pytest.mark.parametrize("S", [3, 40, 290])
+def test_token_major_layout(S):
+    """[S, B, width] storage: the batch stride is the smaller one."""
+    ops = _make(3, S, 64, 96, **FULL, seed=S)
+    for name in ("x", "residual"):
+        ops[name] = ops[name].transpose(0, 1).contiguous().transpose(0, 1)
+    out = torch.empty((S, 3, 96), dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    _run(ops, out=out)
+    R.check(out, R.linear(**ops), "token major")
+
+
+@pytest.mark.parametrize("S", [1, 19, 256, 300, 1100])
+def test_residual_in_place(S):
+    ops = _make(2, S, 200, 264, **FULL, seed=S)
+    ref = R.linear(**ops)
+    apart = _run(ops).clone()
+    got = _run(ops, out=ops["residual"])
+    assert got is ops["residual"]
+    R.check(got, ref, "in place")
+    assert torch.equal(got, apart)
+
+
+@pytest.mark.parametrize("B,S", [(1, 5), (2, 128), (1, 600)])
+def test_two_dimensional_and_broadcast_vectors(B, S):
+    ops = _make(B, S, 64, 64, **FULL, seed=S)
+    one = ops["gate"][0]
+    per_batch = _run(dict(ops, gate=one.expand(B, 64).contiguous()))
+    assert torch.equal(_run(dict(ops, gate=one)), per_batch)
+    assert torch.equal(_run(dict(ops, gate=one.expand(B, 64))), per_batch)
+    if B == 1:
+        flat = _run(dict(ops, x=ops["x"][0], residual=ops["residual"][0]))
+        assert flat.shape == (S, 64) and torch.equal(flat, per_batch[0])
+
+
+@pytest.mark.parametrize("S", [1, 30, 200, 257, 900])
+def test_same_bits_every_time_and_rows_do_not_mix(S):
+    """Rows with infinities and NaN leave the others' bits alone; infinities and
+    NaN in a feature's weights stay in that feature."""
+    ops = _make(1, S, 1032, 264, **FULL, act="silu", seed=S)
+    first = _run(ops).clone()
+    assert torch.equal(_run(ops), first)
+    if S > 1:
+        x = ops["x"].clone()
+        x[0, S // 2, 3] = float("nan")
+        x[0, S - 1, 100:] = float("inf")
+        got = _run(dict(ops, x=x))
+        keep = [s for s in range(S) if s not in (S // 2, S - 1)]
+        assert torch.equal(got[0, keep], first[0, keep])
+        assert bool(torch.isnan(got[0, S // 2]).all())
+    w = ops["w"].clone()
+    w[17] = float("inf")
+    w[18] = float("nan")
+    got = _run(dict(ops, w=w))
+    keep = [n for n in range(264) if n not in (17, 18)]
+    assert torch.equal(got[..., keep], first[..., keep])
+    assert not bool(torch.isfinite(got[..., 17:19]).any())
+
+
+def test_gelu_and_silu_far_from_zero():
+    """Arguments far out on both sides: act(y) is y or 0 there, never NaN."""
+    x = torch.zeros(1, 4, 64, device="cuda").bfloat16()
+    x[0, :, 0] = torch.tensor([-3e4, -100.0, 100.0, 3e4]).bfloat16()
+    w = torch.eye(64, device="cuda").bfloat16()
+    for S, pad in ((4, 0), (300, 296)):
+        xs = torch.cat([x, x.new_zeros(1, pad, 64)], 1)
+        for act in ("silu", "gelu_tanh"):
+            ops = dict(x=xs, w=w, act=act)
+            got = _run(ops)
+            R.check(got, R.linear(**ops), act)
+
+
+@pytest.mark.parametrize("S", [4, 700])
+def test_on_another_stream_and_in_a_graph(S):
+    ops = _make(1, S, 264, 136, **FULL, seed=S)
+    ref = R.linear(**ops)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [binding.linear(**ops, stream=side) for _ in range(3)]
+    side.synchronize()
+    for o in outs:
+        R.check(o, ref, "side stream")
+    # a captured call reads its inputs anew at every replay; two graphs at once
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [torch.empty_like(outs[0]) for _ in range(2)]
+    graphs = []
+    for o in outs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            binding.linear(**ops, out=o, status=status)
+    other = _make(1, S, 264, 136, **FULL, seed=S + 1)
+    for k in ("x", "w", "bias", "gate", "residual"):
+        ops[k].copy_(other[k])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        graphs[0].replay()
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    ref = R.linear(**ops)
+    for o in outs:
+        R.check(o, ref, "graph")
+    assert int(status.item()) == 0
+
+
+def test_offsets_past_32_bits():
+    """2.4e9 output elements, and a batch stride of as many: sampled rows."""
+    S, K, N = 300_000, 64, 8192
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(1, S, K, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(N, K, generator=g, device="cuda") / 8).bfloat16()
+    out = _run(dict(x=x, w=w))
+    rows = torch.tensor([0, 131_071, 262_143, 262_145, S - 2, S - 1], device="cuda")
+    R.check(out[:, rows], R.linear(x[:, rows], w), "far rows")
+    # few rows per batch element, the second one 2.4e9 elements behind the first
+    far = out.view(-1)[: 2 * (S // 2) * N].view(2, S // 2, N)[:, :7]
+    res = far.clone()
+    xs = torch.randn(2, 7, K, generator=g, device="cuda").bfloat16()
+    _run(dict(x=xs, w=w, residual=far), out=far)
+    R.check(far, R.linear(xs, w, residual=res), "far batch element")
+
+
+def test_refusals():
+    ops = _make(2, 5, 64, 72, **FULL)
+    bad = [
+        dict(act="relu"), dict(x=ops["x"].float()), dict(w=ops["w"].float()),
+        dict(w=ops["w"][:, :56]), dict(x=ops["x"][..., ::2]), dict(x=ops["x"][:, :, None]),
+        dict(x2=ops["x"]), dict(bias=ops["bias"][:64]), dict(bias=ops["bias"].float()),
+        dict(bias=ops["bias"].double(), gate=None), dict(gate=ops["gate"][:, :64]),
+        dict(gate=torch.cat([ops["gate"]] * 2)), dict(residual=ops["residual"][:, :4]),
+        dict(residual=ops["residual"].float()), dict(w=ops["w"].cpu()),
+        dict(residual=ops["residual"].cpu()), dict(gate=ops["gate"].cpu()),
+        dict(w=ops["w"][:71], act="swiglu"),
+    ]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            binding.linear(**dict(ops, **kw))
+    for kw, code in (
+        (dict(x=ops["x"][:1].expand(2, 5, 64)), -2),            # batch stride 0
+        (dict(x=ops["x"][:, :1].expand(2, 5, 64)), -2),         # token stride 0
+        (dict(w=ops["w"][:70], bias=None, gate=None, residual=None), -2),
+        (dict(x=torch.zeros(2, 5, 72, device="cuda").bfloat16()[..., 4:68]), -4),
+        (dict(x=torch.zeros(2, 0, 64, device="cuda").bfloat16(), residual=None), None),
+    ):
+        with pytest.raises(binding.FluxError) as e:
+            binding.linear(**dict(ops, **kw))
+        assert code is None or e.value.status == code
+    with pytest.raises(ValueError):
+        binding.linear(**ops, out=torch.empty(2, 5, 64, device="cuda").bfloat16())
+    with pytest.raises(ValueError):
+        binding.linear(**ops, status=torch.zeros(1, device="cuda"))
+    with pytest.raises(binding.FluxError) as e:
+        binding.linear(**dict(ops, x=ops["x"], w=ops["w"][:64], bias=None, gate=None,
+                              residual=None), out=ops["x"])
+    assert e.value.status == -9
