@@ -632,31 +632,31 @@ NORMS = {"layer": 0, "rms": 1}
 def _token_rows(name, t, shape, dtype, device):
     """(address, batch stride, token stride) of a tensor of token rows, [B, S,
     width] or [S, width] with contiguous channels; raises for anything else."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
     st = t.stride()
-    if st[-1] != 1:
+    if t.shape != shape or t.dtype != dtype or t.device != device or st[-1] != 1:
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
         raise ValueError(f"{name} must have contiguous channels, got strides {st}")
-    return t.data_ptr(), (st[0] if len(st) == 3 else 0), st[-2]
+    return (t.data_ptr(), st[0], st[1]) if len(st) == 3 else (t.data_ptr(), 0, st[0])
 
 
 def _vector(name, t, B, width, dtype, device):
     """(address, batch stride) of a vector [width], or of one per batch element
     [B, width] (a stride of 0 where all are the same)."""
-    if t.shape[-1:] != (width,) or t.dim() > 2 or (t.dim() == 2 and t.shape[0] not in (1, B)):
-        raise ValueError(f"{name} must be [{width}] or [{B}, {width}], got {tuple(t.shape)}")
+    shape, st = t.shape, t.stride()
+    if shape[-1:] != (width,) or len(shape) > 2 or (len(shape) == 2 and shape[0] not in (1, B)):
+        raise ValueError(f"{name} must be [{width}] or [{B}, {width}], got {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    st = t.stride()
     if width > 1 and st[-1] != 1:
         raise ValueError(f"{name} must be contiguous, got strides {st}")
-    return t.data_ptr(), (st[0] if t.dim() == 2 and t.shape[0] == B and B > 1 else 0)
+    return t.data_ptr(), (st[0] if len(shape) == 2 and shape[0] == B and B > 1 else 0)
 
 
 def _vector_type(names, vecs):
@@ -676,19 +676,30 @@ def _vector_type(names, vecs):
 
 
 def _stream_of(x, stream):
-    """(the stream, its handle) for a call on x's device, which must be current."""
+    """The handle of the stream of a call on x's device, which must be current."""
     import torch
 
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor (no CPU path exists)")
-    cur = torch.cuda.current_stream()
-    if x.device.index != cur.device_index:
-        raise ValueError(f"x is on {x.device}, the current device is {cur.device}")
+    dev = torch.cuda.current_device()
+    if x.get_device() != dev:
+        raise ValueError(f"x is on {x.device}, the current device is cuda:{dev}")
     if stream is None:
-        stream = cur
-    elif stream.device_index != cur.device_index:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
         raise ValueError(f"the stream is on {stream.device}, x on {x.device}")
-    return stream, stream.cuda_stream
+    return stream.cuda_stream
+
+
+def _allocate(stream, fn, *args, **kw):
+    """Memory of the stream that uses it: fn(*args) under `stream` (None: the
+    current one)."""
+    import torch
+
+    if stream is None:
+        return fn(*args, **kw)
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 def linear(x, w, x2=None, bias=None, act=None, gate=None, residual=None, out=None, status=None,
@@ -707,7 +718,7 @@ def linear(x, w, x2=None, bias=None, act=None, gate=None, residual=None, out=Non
     import torch
 
     lib = load()
-    stream, handle = _stream_of(x, stream)
+    handle = _stream_of(x, stream)
     dev, bf16 = x.device, torch.bfloat16
     if x.dim() not in (2, 3):
         raise ValueError(f"x must be [B, S, K] or [S, K], got {tuple(x.shape)}")
@@ -732,12 +743,10 @@ def linear(x, w, x2=None, bias=None, act=None, gate=None, residual=None, out=Non
     vt, vec_f32 = _vector_type(("bias", "gate"), (bias, gate))
     bp = _vector("bias", bias, 1, rows, vt, dev)[0] if bias is not None else None
     gp, gb = _vector("gate", gate, B, N, vt, dev) if gate is not None else (None, 0)
-    if out is None or status is None:
-        with torch.cuda.stream(stream):  # memory of the stream that uses it
-            if out is None:
-                out = torch.empty(shape, dtype=bf16, device=dev)
-            if status is None:
-                status = torch.zeros(1, dtype=torch.int32, device=dev)
+    if out is None:
+        out = _allocate(stream, torch.empty, shape, dtype=bf16, device=dev)
+    if status is None:
+        status = _allocate(stream, torch.zeros, 1, dtype=torch.int32, device=dev)
     op, ob, orow = _token_rows("out", out, shape, bf16, dev)
     if status.dtype != torch.int32 or status.numel() < 1 or status.device != dev:
         raise ValueError(f"status must hold one int32 on {dev}")
@@ -762,7 +771,7 @@ def modulated_norm(x, scale=None, shift=None, y=None, gate=None, norm="layer", e
     import torch
 
     lib = load()
-    stream, handle = _stream_of(x, stream)
+    handle = _stream_of(x, stream)
     dev, bf16 = x.device, torch.bfloat16
     if x.dim() not in (2, 3):
         raise ValueError(f"x must be [B, S, dim] or [S, dim], got {tuple(x.shape)}")
@@ -779,12 +788,10 @@ def modulated_norm(x, scale=None, shift=None, y=None, gate=None, norm="layer", e
     sp, sb = _vector("scale", scale, B, dim, vt, dev) if scale is not None else (None, 0)
     fp, fb = _vector("shift", shift, B, dim, vt, dev) if shift is not None else (None, 0)
     gp, gb = _vector("gate", gate, B, dim, vt, dev) if gate is not None else (None, 0)
-    if out is None or (y is not None and x_out is None):
-        with torch.cuda.stream(stream):  # memory of the stream that uses it
-            if out is None:
-                out = torch.empty(shape, dtype=bf16, device=dev)
-            if y is not None and x_out is None:
-                x_out = torch.empty(shape, dtype=x.dtype, device=dev)
+    if out is None:
+        out = _allocate(stream, torch.empty, shape, dtype=bf16, device=dev)
+    if y is not None and x_out is None:
+        x_out = _allocate(stream, torch.empty, shape, dtype=x.dtype, device=dev)
     hp, hb, hr = _token_rows("out", out, shape, bf16, dev)
     yp, yb, yr = _token_rows("y", y, shape, bf16, dev) if y is not None else (None, 0, 0)
     op, ob, orow = (_token_rows("x_out", x_out, shape, x.dtype, dev) if y is not None
