@@ -157,10 +157,13 @@ int flux_linear(const void *x, int64_t x_bs, int64_t x_rs, int K, const void *x2
     q.B = 1;
     q.S = B * S;
   }
-  const bool few = q.B * ((q.S + 7) / 8 * 8) <= flux::kLinearRowsMax;
-  const cudaError_t e =
-      few ? flux::launch_linear_rows(q, epi, act, status, static_cast<cudaStream_t>(stream))
-          : flux::launch_linear_pair(q, epi, act, status, static_cast<cudaStream_t>(stream));
+  const int sms = flux::sm_count_current_device();
+  const flux::SplitPlan split = flux::plan_split(q, act, sms);
+  const flux::PairPlan pair = flux::plan_pair(q, act, sms);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = split.ns < pair.ns
+                            ? flux::launch_linear_split(q, split, epi, act, status, st)
+                            : flux::launch_linear_pair(q, pair, epi, act, status, st);
   return e == cudaSuccess ? FLUX_OK : FLUX_ERR_CUDA;
 }
 

@@ -149,13 +149,28 @@ struct LinearProblem {
 };
 struct LinearEpilogue;
 
-// The two kernels behind flux_linear (act: a flux_activation). _pair is for
-// any number of rows; _rows takes B * roundup(S, 8) <= kLinearRowsMax.
-constexpr int kLinearRowsMax = 256;
-cudaError_t launch_linear_pair(const LinearProblem &q, const LinearEpilogue &epi, int act,
-                               int *status, cudaStream_t stream);
-cudaError_t launch_linear_rows(const LinearProblem &q, const LinearEpilogue &epi, int act,
-                               int *status, cudaStream_t stream);
+// How linear_split runs a problem: token rows as P (else W rows), the 256 x Q
+// tile, the CTA pairs that split its channels, the ring; how linear_pair does:
+// the tile's width. Both with an estimate of the time in ns.
+struct SplitPlan {
+  bool tokens_p;
+  int Q, C, stages;
+  double ns;
+};
+struct PairPlan {
+  int tn;
+  double ns;
+};
+SplitPlan plan_split(const LinearProblem &q, int act, int sms);
+PairPlan plan_pair(const LinearProblem &q, int act, int sms);
+
+// The two kernels behind flux_linear (act: a flux_activation).
+cudaError_t launch_linear_pair(const LinearProblem &q, const PairPlan &plan,
+                               const LinearEpilogue &epi, int act, int *status,
+                               cudaStream_t stream);
+cudaError_t launch_linear_split(const LinearProblem &q, const SplitPlan &plan,
+                                const LinearEpilogue &epi, int act, int *status,
+                                cudaStream_t stream);
 
 // x_out = x + gate * y, h = norm(x_out) * (1 + scale) + shift over tokens
 // [B, S] of `dim` channels. x and x_out are bf16, or fp32 with stream_f32; y

@@ -25,33 +25,50 @@ struct LinearEpilogue {
 };
 
 // act(y) in fp32. SiLU y / (1 + e^-y); GELU in its tanh form, of which
-// 0.5 (1 + tanh u) = 1 / (1 + e^-2u) needs one exponential.
+// 0.5 (1 + tanh u) = 1 / (1 + e^-2u) needs one exponential. The fast division
+// is off by two fp32 steps (and gives 0 where the divisor passes 2^126, as the
+// quotient's bf16 does): an epilogue with the exact one took twice as long.
 template <int kAct>
 __device__ __forceinline__ float activate(float y) {
   if constexpr (kAct == FLUX_ACT_SILU) {
-    return y / (1.f + __expf(-y));
+    return __fdividef(y, 1.f + __expf(-y));
   } else if constexpr (kAct == FLUX_ACT_GELU_TANH) {
     const float u2 = 1.5957691216057308f * (y + 0.044715f * y * y * y);  // 2 sqrt(2/pi) (...)
-    return y / (1.f + __expf(-u2));
+    return __fdividef(y, 1.f + __expf(-u2));
   } else {
     return y;
   }
 }
 
-// Eight consecutive entries of a bf16 or fp32 vector, 16-byte aligned.
+// Eight consecutive entries of a bf16 or fp32 vector, 16-byte aligned. (Plain
+// loads: a launch that overlaps the end of the kernel before it must not take
+// the read-only path to what that kernel may have written.)
 __device__ __forceinline__ void load_vec8(const void *base, int64_t off, int f32, float (&v)[8]) {
   if (f32) {
     const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
+    const float4 a = p[0], b = p[1];
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off));
+    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off);
     v[0] = bf16lo_to_f32(w.x), v[1] = bf16hi_to_f32(w.x);
     v[2] = bf16lo_to_f32(w.y), v[3] = bf16hi_to_f32(w.y);
     v[4] = bf16lo_to_f32(w.z), v[5] = bf16hi_to_f32(w.z);
     v[6] = bf16lo_to_f32(w.w), v[7] = bf16hi_to_f32(w.w);
   }
+}
+
+// Four entries, 8-byte (bf16) or 16-byte (fp32) aligned.
+__device__ __forceinline__ float4 load_vec4(const void *base, int64_t off, int f32) {
+  if (f32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
+  const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + off);
+  return make_float4(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x), bf16lo_to_f32(w.y),
+                     bf16hi_to_f32(w.y));
+}
+
+__device__ __forceinline__ float load_vec1(const void *base, int64_t off, int f32) {
+  return f32 ? static_cast<const float *>(base)[off]
+             : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(base)[off]) << 16);
 }
 
 __device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
@@ -66,39 +83,14 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 
-// Eight features f .. f + 7 of one token through the epilogue, from the
-// accumulators a (and, for SwiGLU, u: the linear half), rounded once to bf16.
-// SwiGLU's bias holds the gate half's N entries, then the linear half's.
-template <int kAct>
-__device__ __forceinline__ uint4 finish8(const LinearEpilogue &e, int64_t N, int64_t f,
-                                         int64_t gate_row, const float (&a)[8],
-                                         const float (&u)[8], bool has_res, uint4 res) {
-  float y[8], b[8] = {};
-  if (e.bias != nullptr) load_vec8(e.bias, f, e.vec_f32, b);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = a[i] + b[i];
-  if constexpr (kAct == FLUX_ACT_SWIGLU) {
-    float bu[8] = {};
-    if (e.bias != nullptr) load_vec8(e.bias, N + f, e.vec_f32, bu);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = activate<FLUX_ACT_SILU>(y[i]) * (u[i] + bu[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = activate<kAct>(y[i]);
-  }
-  if (e.gate != nullptr) {
-    float g[8];
-    load_vec8(e.gate, gate_row * e.gate_bs + f, e.vec_f32, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] *= g[i];
-  }
-  if (has_res) {
-    float r[8];
-    unpack8(res, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] += r[i];
-  }
-  return pack8(y);
+// What the plans' estimates (ns) share: an SM takes in about 112 bytes per ns;
+// a stage's 64 channels are four MMAs of N / 2 cycles, about N ns. Fitted, like
+// the constants beside them, to 1400 timings of 50 problems from 1 to 4608
+// rows: the form that the estimates pick takes 1.01 times the best one's time
+// (geometric mean; at most 1.12).
+constexpr double kBytesPerNs = 112.0;
+inline double stage_ns(double bytes, int n) {
+  return bytes / kBytesPerNs > n ? bytes / kBytesPerNs : n;
 }
 
 // A 3-D tensor map over bf16 rows [B, S, cols] with the given element

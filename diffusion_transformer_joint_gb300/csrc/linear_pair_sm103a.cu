@@ -23,20 +23,28 @@
 // so that the pairs running at the same time form a block of about kGroup row
 // blocks x (pairs / kGroup) feature tiles and share both operands in L2.
 //
-// 8 warps per CTA:
-//   warp 0: TMA producer (6-stage ring);
+// 12 warps per CTA:
+//   warp 0: TMA producer (a ring of 192 KB: six stages of a 256-column tile, up
+//   to ten of narrower ones: a copy takes about 1.5 us to land, so the bytes on
+//   their way bound what a CTA draws);
 //   warp 1: MMA issuer in the even CTA (whole warp, elect.sync issues);
 //   warp 2: TMEM allocation (two 256-column accumulators, pair-wide);
-//   warps 4-7: epilogue, one TMEM lane (token row) per thread, 32 features at
-//   a time. A warp stages its 32 rows x 32 features in a 2 KB box (64-byte
-//   swizzle, a ring of four per warp). With a residual the box is first filled
-//   by a TMA copy of the residual, issued two boxes ahead (the first two of a
-//   tile before its accumulator is waited for), and updated in place; lane 0
-//   stores the box with one TMA copy. Rows past S and features past N are
-//   neither read nor written.
+//   warps 4-11: epilogue, one TMEM lane (token row) per thread, 32 features at
+//   a time, two warps per lane quadrant taking turns. The tile's bias and gate
+//   are staged in shared memory as fp32 while its MMAs run. A warp stages its
+//   32 rows x 32 features in one of two 2 KB boxes (64-byte swizzle). With a
+//   residual the box is first filled by a TMA copy of the residual, issued a
+//   box ahead (the first two of a tile before its accumulator is waited for),
+//   and updated in place; lane 0 stores the box with one TMA copy. Rows past S
+//   and features past N are neither read nor written.
 // The two accumulators let the epilogue of one tile overlap the next tile's
-// MMAs. Every wait is bounded; a wait that runs out aborts the CTA and sets
-// the status word to FLUX_ERR_DEVICE_TIMEOUT.
+// MMAs; the last tile's is what a call pays for (with four warps, each reading
+// bias and gate from global memory, 10 us of the 83 that 4096 rows of 4096 -> 4096 channels took).
+//
+// The launch overlaps its prologue with the end of the kernel before it in the
+// stream (programmatic dependent launch): what reads or writes global memory
+// waits for that kernel first. Every wait is bounded; a wait that runs out
+// aborts the CTA and sets the status word to FLUX_ERR_DEVICE_TIMEOUT.
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -49,32 +57,34 @@ namespace {
 constexpr int kRows = 128;  // token rows per CTA (256 per pair)
 constexpr int kMaxTn = 256;
 constexpr int kK = 64;  // channels per stage
-constexpr int kStages = 6;
+constexpr uint32_t kRingBytes = 6 * 32768;  // of stages: 6 of the widest tile's, up to 10
+constexpr int kMaxStages = 10;
 constexpr int kGroup = 9;
-constexpr uint32_t kABytes = kRows * kK * 2;         // 16 KB: this CTA's token rows
-constexpr uint32_t kBBytes = kMaxTn / 2 * kK * 2;    // up to 16 KB: its half of the W rows
-constexpr uint32_t kStageBytes = kABytes + kBBytes;
-constexpr int kThreads = 256;
-constexpr int kBoxes = 4;                 // boxes per epilogue warp
+constexpr uint32_t kABytes = kRows * kK * 2;  // 16 KB: this CTA's token rows
+constexpr uint32_t kBRowBytes = kK * 2;       // a W row of its half of the tile
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kBoxes = 2;                 // boxes per epilogue warp
 constexpr uint32_t kBoxBytes = 32 * 64;   // 32 rows x 32 features
 constexpr int kBarFull = 0;               // (even CTA) both CTAs' copies landed
-constexpr int kBarEmpty = kStages;        // the pair's MMAs read the stage
-constexpr int kBarAccFull = 2 * kStages;
+constexpr int kBarEmpty = kMaxStages;     // the pair's MMAs read the stage
+constexpr int kBarAccFull = 2 * kMaxStages;
 constexpr int kBarAccEmpty = kBarAccFull + 2;  // (even CTA) both epilogues read it
 constexpr int kBarDrain = kBarAccEmpty + 2;
 constexpr int kBarRes = kBarDrain + 1;  // residual box landed, per warp and box
-constexpr int kNumBars = kBarRes + 4 * kBoxes;
-constexpr uint32_t kOffBox = kStages * kStageBytes;
-constexpr uint32_t kOffBar = kOffBox + 4 * kBoxes * kBoxBytes;
+constexpr int kNumBars = kBarRes + kEpiWarps * kBoxes;
+constexpr uint32_t kOffBox = kRingBytes;
+constexpr uint32_t kOffVec = kOffBox + kEpiWarps * kBoxes * kBoxBytes;  // a tile's bias, gate
+constexpr uint32_t kOffBar = kOffVec + 2 * kMaxTn * 4;
 constexpr uint32_t kOffTmemSlot = kOffBar + 8 * kNumBars;
 constexpr uint32_t kOffAbort = kOffTmemSlot + 8;
-constexpr uint32_t kSmemBytes = kOffAbort + 8 + 1024;  // + slack for 1024-byte alignment
+constexpr uint32_t kSmemBytes = kOffAbort + 8;
 static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 constexpr uint16_t kPairMask = 0x3;
 
 struct PairShape {
   int64_t S, N;
-  int tn, nk1, nk;            // tile width; stages of x; stages in all
+  int tn, stages, nk1, nk;        // tile width; ring; stages of x, in all
   int n_sb, n_rb, n_ft, n_tiles;  // row blocks per batch element, in all; feature tiles
 };
 
@@ -99,14 +109,29 @@ __device__ __forceinline__ void bounded(uint32_t bar, uint32_t parity) {
   }
 }
 
+// The epilogue warps only.
+__device__ __forceinline__ void epi_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
+}
+
+__device__ __forceinline__ void read8(float (&v)[8], const float *p) {
+  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void add8(float (&v)[8], const float *p) {
+  float w[8];
+  read8(w, p);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += w[i];
+}
+
 template <int kAct>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ PairMaps maps, const PairShape p,
                        const LinearEpilogue epi, const int has_res, int *__restrict__ status) {
   constexpr bool kGlu = kAct == FLUX_ACT_SWIGLU;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t base[];
   const uint32_t sbase = smem_addr(base);
   auto bar = [&](int i) { return sbase + kOffBar + 8u * static_cast<uint32_t>(i); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + kOffTmemSlot);
@@ -118,18 +143,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cid = static_cast<int>(cluster_id_x());
   const int ncl = static_cast<int>(cluster_count_x());
   const int feats = kGlu ? p.tn / 2 : p.tn;  // output features per tile
+  const uint32_t stage_bytes = kABytes + static_cast<uint32_t>(p.tn / 2) * kBRowBytes;
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < p.stages; ++s) {
       mbar_init(bar(kBarFull + s), 1);
       mbar_init(bar(kBarEmpty + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar(kBarAccFull + b), 1);
-      mbar_init(bar(kBarAccEmpty + b), 8);  // four epilogue warps of each CTA
+      mbar_init(bar(kBarAccEmpty + b), 2 * kEpiWarps);  // the epilogue warps of both CTAs
     }
     mbar_init(bar(kBarDrain), 1);
-    for (int i = 0; i < 4 * kBoxes; ++i) mbar_init(bar(kBarRes + i), 1);
+    for (int i = 0; i < kEpiWarps * kBoxes; ++i) mbar_init(bar(kBarRes + i), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -143,12 +169,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  grid_dep_launch_dependents();
 
   if (warp == 0 && lane == 0) {
     // ---------------------------------------------------------- TMA producer
-    const uint32_t bytes = kABytes + static_cast<uint32_t>(p.tn / 2) * kK * 2;
-    int it = 0;  // stages filled so far
+    tma_prefetch_desc(&maps.x);
+    tma_prefetch_desc(&maps.w);
+    int s = 0;          // stage
+    uint32_t turn = 0;  // times round the ring
     bool ok = true;
+    grid_dep_wait();
     for (int t = cid; ok && t < p.n_tiles; t += ncl) {
       int ft, rb;
       tile_at(p, t, ft, rb);
@@ -158,30 +188,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the odd CTA's: the second half, or the linear features
       const int64_t f0 = static_cast<int64_t>(ft) * feats;
       const int rw = static_cast<int>(crank == 0 ? f0 : kGlu ? p.N + f0 : f0 + p.tn / 2);
-      for (int ks = 0; ks < p.nk; ++ks, ++it) {
-        const int s = it % kStages;
-        const uint32_t use = static_cast<uint32_t>(it / kStages);
-        if (!(ok = mbar_wait_cluster(bar(kBarEmpty + s), (use & 1u) ^ 1u, abort_flag))) break;
-        const uint32_t dst = sbase + s * kStageBytes;
+      for (int ks = 0; ks < p.nk; ++ks) {
+        if (!(ok = mbar_wait_cluster(bar(kBarEmpty + s), (turn & 1u) ^ 1u, abort_flag))) break;
+        const uint32_t dst = sbase + s * stage_bytes;
         // both CTAs' copies complete on the even CTA's stage barrier
-        if (crank == 0) mbar_arrive_expect_tx(bar(kBarFull + s), 2 * bytes);
+        if (crank == 0) mbar_arrive_expect_tx(bar(kBarFull + s), 2 * stage_bytes);
         const uint32_t full0 = mapa_shared(bar(kBarFull + s), 0);
         const bool first = ks < p.nk1;
         const int c = (first ? ks : ks - p.nk1) * kK;
         tma_load_3d_pair(dst, first ? &maps.x : &maps.x2, full0, c, s0, b);
         tma_load_3d_pair(dst + kABytes, first ? &maps.w : &maps.w2, full0, c, rw, 0);
+        if (++s == p.stages) s = 0, ++turn;
       }
     }
     // every copy of the pair has landed before the CTAs exit (the even CTA's
     // stage barriers count both CTAs' copies; the final cluster barrier
     // keeps the odd CTA until then)
-    if (crank == 0)
-      for (int j = (it > kStages ? it - kStages : 0); j < it; ++j)
-        bounded(bar(kBarFull + j % kStages), static_cast<uint32_t>(j / kStages) & 1u);
+    if (crank == 0) {
+      for (int i = 0; i < p.stages; ++i) {
+        // the stage's last use, if any, was in this turn or the one before
+        if (i < s)
+          bounded(bar(kBarFull + i), turn & 1u);
+        else if (turn > 0)
+          bounded(bar(kBarFull + i), (turn - 1) & 1u);
+      }
+    }
   } else if (warp == 1 && crank == 0) {
     // ------------------------------------------------ MMA issuer (even CTA)
     const uint32_t idesc = idesc_bf16_f32(2 * kRows, p.tn, 0, 0);
-    int it = 0;
+    int s = 0;
+    uint32_t turn = 0;
     int lt = 0;
     bool ok = true;
     for (int t = cid; ok && t < p.n_tiles; t += ncl, ++lt) {
@@ -192,20 +228,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       tc_fence_after_sync();
       const uint32_t d = tmem + static_cast<uint32_t>(buf * kMaxTn);
-      for (int ks = 0; ks < p.nk; ++ks, ++it) {
-        const int s = it % kStages;
-        const uint32_t par = static_cast<uint32_t>(it / kStages) & 1u;
+      for (int ks = 0; ks < p.nk; ++ks) {
         if (!(ok = __all_sync(0xffffffffu,
-                              mbar_wait_cluster(bar(kBarFull + s), par, abort_flag))))
+                              mbar_wait_cluster(bar(kBarFull + s), turn & 1u, abort_flag))))
           break;
         tc_fence_after_sync();
-        const uint64_t da = sdesc_sw128(sbase + s * kStageBytes, 16, 1024);
-        const uint64_t db = sdesc_sw128(sbase + s * kStageBytes + kABytes, 16, 1024);
+        const uint64_t da = sdesc_sw128(sbase + s * stage_bytes, 16, 1024);
+        const uint64_t db = sdesc_sw128(sbase + s * stage_bytes + kABytes, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < kK / 16; ++kk)
           mma_ss_pair_elect(d, desc_advance(da, kk * 32), desc_advance(db, kk * 32), idesc,
                             (ks | kk) != 0 ? 1u : 0u);
         mma_commit_pair_elect(bar(kBarEmpty + s), kPairMask);  // both CTAs may refill
+        if (++s == p.stages) s = 0, ++turn;
       }
       if (!ok) break;
       mma_commit_pair_elect(bar(kBarAccFull + buf), kPairMask);  // both accumulators complete
@@ -216,40 +251,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
-    const int wq = warp & 3;  // TMEM lane quadrant
+    const int wq = warp & 3;         // TMEM lane quadrant
+    const int turn = (warp - 4) >> 2;  // takes the boxes of this parity
+    const int et = tid - 128;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t acc_empty0 = mapa_shared(bar(kBarAccEmpty), 0);
-    const uint32_t boxes = sbase + kOffBox + static_cast<uint32_t>(wq) * kBoxes * kBoxBytes;
-    const int bar_res = kBarRes + wq * kBoxes;
+    const uint32_t boxes = sbase + kOffBox + static_cast<uint32_t>(warp - 4) * kBoxes * kBoxBytes;
+    const int bar_res = kBarRes + (warp - 4) * kBoxes;
+    float *vec_bias = reinterpret_cast<float *>(base + kOffVec);
+    float *vec_gate = vec_bias + kMaxTn;
     uint32_t n_loaded = 0, n_stored = 0;  // boxes of this warp whose residual was asked for / staged
     int lt = 0;
     bool ok = true;
+    grid_dep_wait();
     for (int t = cid; ok && t < p.n_tiles; t += ncl, ++lt) {
       int ft, rb;
       tile_at(p, t, ft, rb);
       const int b = rb / p.n_sb;
-      const int s0 = (rb - b * p.n_sb) * (2 * kRows) + static_cast<int>(crank) * kRows + wq * 32;
+      const int sc = (rb - b * p.n_sb) * (2 * kRows) + static_cast<int>(crank) * kRows;
+      const int s0 = sc + wq * 32;
       const int64_t f0 = static_cast<int64_t>(ft) * feats;
       const int64_t left = p.N - f0;
       // boxes of this tile that hold anything to write
       const int n_box = s0 >= p.S ? 0
                                   : static_cast<int>(left < feats ? (left + 31) / 32 : feats / 32);
-      const int64_t row = static_cast<int64_t>(b) * p.S + (s0 + lane < p.S ? s0 + lane : p.S - 1);
-      const int64_t gate_row = epi.gate != nullptr ? row / epi.gate_rows : 0;
-      // the residual of box c: its buffer was last stored from kBoxes boxes
-      // ago, at most one later store may still be reading
+      // the residual of box c goes to the buffer of this warp's box before
+      // last, whose store has read it
       auto load_residual = [&](int c) {
         const uint32_t slot = n_loaded % kBoxes;
         if (lane == 0) {
-          bulk_wait_read_1();
           mbar_arrive_expect_tx(bar(bar_res + slot), kBoxBytes);
           tma_load_3d(boxes + slot * kBoxBytes, &maps.res, bar(bar_res + slot),
                       static_cast<int>(f0) + c * 32, s0, b);
         }
         ++n_loaded;
       };
-      if (has_res)
-        for (int c = 0; c < 2 && c < n_box; ++c) load_residual(c);
+      if (has_res) {
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+        for (int c = turn; c < n_box && c < turn + 2 * kBoxes; c += 2) load_residual(c);
+      }
+      // bias and gate of the tile, once every warp is done with the last one's
+      // (a gate that changes inside the CTA's rows is read row by row instead)
+      bool gate_rowwise = false;
+      int64_t gate_row = 0;
+      if (epi.gate != nullptr) {
+        const int64_t r0 = static_cast<int64_t>(b) * p.S + (sc < p.S ? sc : p.S - 1);
+        const int64_t r1 = static_cast<int64_t>(b) * p.S + (sc + kRows < p.S ? sc + kRows : p.S) - 1;
+        gate_row = r0 / epi.gate_rows;
+        gate_rowwise = r1 / epi.gate_rows != gate_row;
+      }
+      if (epi.bias != nullptr || epi.gate != nullptr) {
+        epi_barrier();
+        if (epi.bias != nullptr && et < p.tn) {
+          const int64_t f = f0 + (kGlu && et >= feats ? et - feats : et);
+          if (f < p.N)
+            vec_bias[et] = load_vec1(epi.bias, kGlu && et >= feats ? p.N + f : f, epi.vec_f32);
+        }
+        if (epi.gate != nullptr && !gate_rowwise && et < feats && f0 + et < p.N)
+          vec_gate[et] = load_vec1(epi.gate, gate_row * epi.gate_bs + f0 + et, epi.vec_f32);
+        epi_barrier();
+      }
+      if (gate_rowwise) {
+        const int64_t r = static_cast<int64_t>(b) * p.S + (s0 + lane < p.S ? s0 + lane : p.S - 1);
+        gate_row = r / epi.gate_rows;
+      }
       if (!(ok = __all_sync(0xffffffffu,
                             mbar_wait_cluster(bar(kBarAccFull + (lt & 1)),
                                               (static_cast<uint32_t>(lt) >> 1) & 1u, abort_flag))))
@@ -257,19 +323,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after_sync();
       const uint32_t tacc = tmem + static_cast<uint32_t>((lt & 1) * kMaxTn) + lane_off;
 #pragma unroll 1
-      for (int c = 0; c < n_box; ++c) {
+      for (int c = turn; c < n_box; c += 2) {
         const uint32_t slot = n_stored % kBoxes;
         const uint32_t box = boxes + slot * kBoxBytes;
         uint32_t a[32], u[32];
         tmem_ld32(tacc + c * 32, a);
         if constexpr (kGlu) tmem_ld32(tacc + feats + c * 32, u);
         if (has_res) {
-          if (c + 2 < n_box) load_residual(c + 2);
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(bar_res + slot),
                                                        (n_stored / kBoxes) & 1u, abort_flag))))
             break;
         } else {
-          if (lane == 0) bulk_wait_read_3();
+          if (lane == 0) bulk_wait_read_1();
           __syncwarp();
         }
         tmem_ld_wait();
@@ -278,15 +343,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t f = f0 + c * 32 + g * 8;
           const uint32_t at = box + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4);
           if (f < p.N) {
-            float av[8], uv[8];
+            const int v0 = c * 32 + g * 8;  // in the tile's vectors
+            float y[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              av[i] = __uint_as_float(a[g * 8 + i]);
-              uv[i] = kGlu ? __uint_as_float(u[g * 8 + i]) : 0.f;
+            for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(a[g * 8 + i]);
+            if (epi.bias != nullptr) add8(y, vec_bias + v0);
+            if constexpr (kGlu) {
+              float w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = __uint_as_float(u[g * 8 + i]);
+              if (epi.bias != nullptr) add8(w, vec_bias + feats + v0);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = activate<FLUX_ACT_SILU>(y[i]) * w[i];
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = activate<kAct>(y[i]);
             }
-            uint4 res = make_uint4(0, 0, 0, 0);
-            if (has_res) res = ld_shared_v4(at);
-            st_shared_v4(at, finish8<kAct>(epi, p.N, f, gate_row, av, uv, has_res != 0, res));
+            if (epi.gate != nullptr) {
+              float w[8];
+              if (gate_rowwise)
+                load_vec8(epi.gate, gate_row * epi.gate_bs + f, epi.vec_f32, w);
+              else
+                read8(w, vec_gate + v0);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] *= w[i];
+            }
+            if (has_res) {
+              float w[8];
+              unpack8(ld_shared_v4(at), w);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] += w[i];
+            }
+            st_shared_v4(at, pack8(y));
           }
         }
         fence_proxy_async_smem();
@@ -296,12 +384,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           bulk_commit();
         }
         ++n_stored;
+        if (has_res && c + 2 * kBoxes < n_box) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          load_residual(c + 2 * kBoxes);
+        }
       }
       if (!ok) break;
       // this warp's TMEM reads are complete: the accumulator may be reused
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8u * static_cast<uint32_t>((lt & 1)));
+      if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8u * static_cast<uint32_t>(lt & 1));
     }
     if (lane == 0) {
       // residual copies still in flight after an abort, then every output store
@@ -323,26 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *abort_flag) atomicExch(status, FLUX_ERR_DEVICE_TIMEOUT);
 }
 
-// Tile width: the accumulator columns of a tile, a multiple of 32 (64 for
-// SwiGLU). A stage of 64 channels keeps a pair busy for about 256 + tn cycles
-// (its 128 token rows and tn/2 W rows per CTA have to arrive from L2; at
-// tn = 256 the MMAs take the same 512), so a wave of tiles costs 256 + tn and
-// the width with the cheapest sum of waves is taken, the widest among equals.
-int pick_tile(int64_t n_rb, int64_t N, bool glu, int pairs) {
-  const int step = glu ? 64 : 32;
-  int best = kMaxTn;
-  int64_t best_cost = INT64_MAX;
-  for (int tn = kMaxTn; tn >= step; tn -= step) {
-    const int64_t feats = glu ? tn / 2 : tn;
-    const int64_t tiles = n_rb * ((N + feats - 1) / feats);
-    const int64_t cost = (tiles + pairs - 1) / pairs * (256 + tn);
-    if (cost < best_cost) best_cost = cost, best = tn;
-  }
-  return best;
-}
-
 template <int kAct>
-cudaError_t launch(const LinearProblem &q, const LinearEpilogue &epi, int *status,
+cudaError_t launch(const LinearProblem &q, int tn, const LinearEpilogue &epi, int *status,
                    cudaStream_t stream) {
   static std::once_flag attr_once[64];
   static cudaError_t attr_err[64];
@@ -358,11 +433,13 @@ cudaError_t launch(const LinearProblem &q, const LinearEpilogue &epi, int *statu
   });
   if (attr_err[dev] != cudaSuccess) return attr_err[dev];
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
@@ -382,7 +459,7 @@ cudaError_t launch(const LinearProblem &q, const LinearEpilogue &epi, int *statu
   p.N = q.N;
   const int64_t n_sb = (q.S + 2 * kRows - 1) / (2 * kRows);
   const int64_t n_rb = n_sb * q.B;
-  p.tn = pick_tile(n_rb, q.N, glu, np);
+  p.tn = tn;
   const int64_t feats = glu ? p.tn / 2 : p.tn;
   const int64_t n_ft = (q.N + feats - 1) / feats;
   if (n_rb * n_ft > 0x3FFFFFFFLL || n_ft * kGroup > 0x3FFFFFFFLL) return cudaErrorInvalidValue;
@@ -390,6 +467,8 @@ cudaError_t launch(const LinearProblem &q, const LinearEpilogue &epi, int *statu
   p.n_rb = static_cast<int>(n_rb);
   p.n_ft = static_cast<int>(n_ft);
   p.n_tiles = static_cast<int>(n_rb * n_ft);
+  p.stages = static_cast<int>(std::min<uint32_t>(
+      kMaxStages, kRingBytes / (kABytes + static_cast<uint32_t>(p.tn / 2) * kBRowBytes)));
   p.nk1 = (q.K + kK - 1) / kK;
   p.nk = p.nk1 + (q.K2 + kK - 1) / kK;
   const int64_t wr = glu ? 2 * q.N : q.N;
@@ -411,6 +490,7 @@ cudaError_t launch(const LinearProblem &q, const LinearEpilogue &epi, int *statu
       !make_row_map(&maps.res, q.residual, q.N, q.S, q.B, q.r_rs, q.r_bs, 32, 32, 1))
     return cudaErrorInvalidValue;
   const int64_t pairs = p.n_tiles < np ? p.n_tiles : np;
+  cfg.numAttrs = 2;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
   return cudaLaunchKernelEx(&cfg, kernel, maps, p, epi, q.residual != nullptr ? 1 : 0, status);
 }
@@ -438,13 +518,36 @@ bool make_row_map(CUtensorMap *map, const void *base, int64_t cols, int64_t S, i
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_linear_pair(const LinearProblem &q, const LinearEpilogue &epi, int act,
-                               int *status, cudaStream_t stream) {
+// The tile's width: a multiple of 32 accumulator columns (64 for SwiGLU). A
+// wave of tiles costs its stages, so the width decides both how long a wave is
+// and how full the last one: 4096 x 4096 outputs are four full waves of 224
+// columns (79.8 us with 4096 channels), or 3.4 of 256 (81.6 us).
+PairPlan plan_pair(const LinearProblem &q, int act, int sms) {
+  const bool glu = act == FLUX_ACT_SWIGLU;
+  const int64_t n_rb = q.B * ((q.S + 2 * kRows - 1) / (2 * kRows));
+  const double nk = static_cast<double>((q.K + kK - 1) / kK + (q.K2 + kK - 1) / kK);
+  const int64_t pairs = std::max(1, sms / 2);
+  PairPlan best{kMaxTn, 1e30};
+  const int step = glu ? 64 : 32;
+  for (int tn = kMaxTn; tn >= step; tn -= step) {
+    const int64_t feats = glu ? tn / 2 : tn;
+    const int64_t tiles = n_rb * ((q.N + feats - 1) / feats);
+    const double waves = static_cast<double>((tiles + pairs - 1) / pairs);
+    const double ns = waves * (nk * stage_ns(kABytes + tn / 2 * kBRowBytes, tn) + 210.0) +
+                      3300.0 + 8.0 * tn;
+    if (ns < best.ns) best = PairPlan{tn, ns};
+  }
+  return best;
+}
+
+cudaError_t launch_linear_pair(const LinearProblem &q, const PairPlan &plan,
+                               const LinearEpilogue &epi, int act, int *status,
+                               cudaStream_t stream) {
   switch (act) {
-    case FLUX_ACT_NONE: return launch<FLUX_ACT_NONE>(q, epi, status, stream);
-    case FLUX_ACT_SILU: return launch<FLUX_ACT_SILU>(q, epi, status, stream);
-    case FLUX_ACT_GELU_TANH: return launch<FLUX_ACT_GELU_TANH>(q, epi, status, stream);
-    default: return launch<FLUX_ACT_SWIGLU>(q, epi, status, stream);
+    case FLUX_ACT_NONE: return launch<FLUX_ACT_NONE>(q, plan.tn, epi, status, stream);
+    case FLUX_ACT_SILU: return launch<FLUX_ACT_SILU>(q, plan.tn, epi, status, stream);
+    case FLUX_ACT_GELU_TANH: return launch<FLUX_ACT_GELU_TANH>(q, plan.tn, epi, status, stream);
+    default: return launch<FLUX_ACT_SWIGLU>(q, plan.tn, epi, status, stream);
   }
 }
 
