@@ -629,22 +629,23 @@ ACTIVATIONS = {None: 0, "silu": 1, "gelu_tanh": 2, "swiglu": 3}
 NORMS = {"layer": 0, "rms": 1}
 
 
-def _token_rows(name, t, shape, dtype, device):
-    """(address, batch stride, token stride) of a tensor of token rows, [B, S,
-    width] or [S, width] with contiguous channels; raises for anything else."""
+def _token_rows(name, t, shape, dtype, dev):
+    """(address, batch stride, token stride) of a tensor of token rows on CUDA
+    device `dev`, [B, S, width] or [S, width] with contiguous channels; raises
+    for anything else."""
     st = t.stride()
-    if t.shape != shape or t.dtype != dtype or t.device != device or st[-1] != 1:
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or st[-1] != 1:
         if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
         raise ValueError(f"{name} must have contiguous channels, got strides {st}")
-    return (t.data_ptr(), st[0], st[1]) if len(st) == 3 else (t.data_ptr(), 0, st[0])
+    return (t.data_ptr(), *st[:2]) if len(st) == 3 else (t.data_ptr(), 0, st[0])
 
 
-def _vector(name, t, B, width, dtype, device):
+def _vector(name, t, B, width, dtype, dev):
     """(address, batch stride) of a vector [width], or of one per batch element
     [B, width] (a stride of 0 where all are the same)."""
     shape, st = t.shape, t.stride()
@@ -652,8 +653,8 @@ def _vector(name, t, B, width, dtype, device):
         raise ValueError(f"{name} must be [{width}] or [{B}, {width}], got {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if width > 1 and st[-1] != 1:
         raise ValueError(f"{name} must be contiguous, got strides {st}")
     return t.data_ptr(), (st[0] if len(shape) == 2 and shape[0] == B and B > 1 else 0)
@@ -676,19 +677,19 @@ def _vector_type(names, vecs):
 
 
 def _stream_of(x, stream):
-    """The handle of the stream of a call on x's device, which must be current."""
+    """(device index, stream handle) of a call on x's device, which must be current."""
     import torch
 
-    if not x.is_cuda:
+    dev = torch.cuda.current_device() if x.is_cuda else None
+    if dev is None:
         raise ValueError("x must be a CUDA tensor (no CPU path exists)")
-    dev = torch.cuda.current_device()
     if x.get_device() != dev:
         raise ValueError(f"x is on {x.device}, the current device is cuda:{dev}")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
     if stream.device_index != dev:
         raise ValueError(f"the stream is on {stream.device}, x on {x.device}")
-    return stream.cuda_stream
+    return dev, stream.cuda_stream
 
 
 def _allocate(stream, fn, *args, **kw):
@@ -717,41 +718,47 @@ def linear(x, w, x2=None, bias=None, act=None, gate=None, residual=None, out=Non
     """
     import torch
 
-    lib = load()
-    handle = _stream_of(x, stream)
-    dev, bf16 = x.device, torch.bfloat16
-    if x.dim() not in (2, 3):
-        raise ValueError(f"x must be [B, S, K] or [S, K], got {tuple(x.shape)}")
-    if act not in ACTIVATIONS:
+    lib = _lib or load()
+    dev, handle = _stream_of(x, stream)
+    bf16, shape = torch.bfloat16, x.shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"x must be [B, S, K] or [S, K], got {tuple(shape)}")
+    code = ACTIVATIONS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {list(ACTIVATIONS)}, got {act!r}")
-    lead = x.shape[:-1]
-    B, S, K = (1, *x.shape) if x.dim() == 2 else x.shape
-    K2 = 0 if x2 is None else int(x2.shape[-1])
+    B, S, K = shape if len(shape) == 3 else (1, *shape)
+    K2 = 0 if x2 is None else x2.shape[-1]
+    xp, xb, xr = _token_rows("x", x, shape, bf16, dev)
     if w.dim() != 2 or w.shape[1] != K + K2:
         raise ValueError(f"w must be [rows, {K + K2}], got {tuple(w.shape)}")
-    rows = w.shape[0]
-    if act == "swiglu" and rows % 2:
-        raise ValueError(f"w must have two equal halves of rows, got {rows}")
-    N = rows // 2 if act == "swiglu" else rows
-    shape = (*lead, N)
-    xp, xb, xr = _token_rows("x", x, x.shape, bf16, dev)
     wp, _, wr = _token_rows("w", w, w.shape, bf16, dev)
-    x2p, x2b, x2r = (_token_rows("x2", x2, (*lead, K2), bf16, dev) if x2 is not None
-                     else (None, 0, 0))
-    rp, rb, rr = (_token_rows("residual", residual, shape, bf16, dev) if residual is not None
-                  else (None, 0, 0))
-    vt, vec_f32 = _vector_type(("bias", "gate"), (bias, gate))
-    bp = _vector("bias", bias, 1, rows, vt, dev)[0] if bias is not None else None
-    gp, gb = _vector("gate", gate, B, N, vt, dev) if gate is not None else (None, 0)
+    rows = N = w.shape[0]
+    if act == "swiglu":
+        if rows % 2:
+            raise ValueError(f"w must have two equal halves of rows, got {rows}")
+        N = rows // 2
+    shape = (*shape[:-1], N)
+    x2p = bp = gp = rp = None
+    x2b = x2r = gb = vec_f32 = rb = rr = 0
+    if x2 is not None:
+        x2p, x2b, x2r = _token_rows("x2", x2, (*shape[:-1], K2), bf16, dev)
+    if residual is not None:
+        rp, rb, rr = _token_rows("residual", residual, shape, bf16, dev)
+    if bias is not None or gate is not None:
+        vt, vec_f32 = _vector_type(("bias", "gate"), (bias, gate))
+        if bias is not None:
+            bp = _vector("bias", bias, 1, rows, vt, dev)[0]
+        if gate is not None:
+            gp, gb = _vector("gate", gate, B, N, vt, dev)
     if out is None:
-        out = _allocate(stream, torch.empty, shape, dtype=bf16, device=dev)
-    if status is None:
-        status = _allocate(stream, torch.zeros, 1, dtype=torch.int32, device=dev)
+        out = _allocate(stream, torch.empty, shape, dtype=bf16, device=x.device)
     op, ob, orow = _token_rows("out", out, shape, bf16, dev)
-    if status.dtype != torch.int32 or status.numel() < 1 or status.device != dev:
-        raise ValueError(f"status must hold one int32 on {dev}")
-    rc = lib.flux_linear(xp, xb, xr, K, x2p, x2b, x2r, K2, wp, wr, B, S, N, ACTIVATIONS[act], bp,
-                         gp, gb, vec_f32, rp, rb, rr, op, ob, orow, status.data_ptr(), handle)
+    if status is None:
+        status = _allocate(stream, torch.zeros, 1, dtype=torch.int32, device=x.device)
+    elif status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != dev:
+        raise ValueError(f"status must hold one int32 on cuda:{dev}")
+    rc = lib.flux_linear(xp, xb, xr, K, x2p, x2b, x2r, K2, wp, wr, B, S, N, code, bp, gp, gb,
+                         vec_f32, rp, rb, rr, op, ob, orow, status.data_ptr(), handle)
     if rc != 0:
         raise FluxError("flux_linear", rc, lib)
     return out
@@ -770,35 +777,41 @@ def modulated_norm(x, scale=None, shift=None, y=None, gate=None, norm="layer", e
     """
     import torch
 
-    lib = load()
-    handle = _stream_of(x, stream)
-    dev, bf16 = x.device, torch.bfloat16
-    if x.dim() not in (2, 3):
-        raise ValueError(f"x must be [B, S, dim] or [S, dim], got {tuple(x.shape)}")
-    if x.dtype not in (bf16, torch.float32):
-        raise ValueError(f"x must be bfloat16 or float32, got {x.dtype}")
-    if norm not in NORMS:
+    lib = _lib or load()
+    dev, handle = _stream_of(x, stream)
+    bf16, shape, dtype = torch.bfloat16, x.shape, x.dtype
+    if len(shape) not in (2, 3):
+        raise ValueError(f"x must be [B, S, dim] or [S, dim], got {tuple(shape)}")
+    if dtype != bf16 and dtype != torch.float32:
+        raise ValueError(f"x must be bfloat16 or float32, got {dtype}")
+    kind = NORMS.get(norm)
+    if kind is None:
         raise ValueError(f"norm must be one of {list(NORMS)}, got {norm!r}")
-    if y is None and (gate is not None or x_out is not None):
-        raise ValueError("gate and x_out need y")
-    shape = x.shape
-    B, S, dim = (1, *shape) if x.dim() == 2 else shape
-    xp, xb, xr = _token_rows("x", x, shape, x.dtype, dev)
-    vt, vec_f32 = _vector_type(("scale", "shift", "gate"), (scale, shift, gate))
-    sp, sb = _vector("scale", scale, B, dim, vt, dev) if scale is not None else (None, 0)
-    fp, fb = _vector("shift", shift, B, dim, vt, dev) if shift is not None else (None, 0)
-    gp, gb = _vector("gate", gate, B, dim, vt, dev) if gate is not None else (None, 0)
+    B, S, dim = shape if len(shape) == 3 else (1, *shape)
+    xp, xb, xr = _token_rows("x", x, shape, dtype, dev)
+    sp = fp = gp = yp = op = None
+    sb = fb = gb = yb = yr = ob = orow = vec_f32 = 0
+    if scale is not None or shift is not None or gate is not None:
+        vt, vec_f32 = _vector_type(("scale", "shift", "gate"), (scale, shift, gate))
+        if scale is not None:
+            sp, sb = _vector("scale", scale, B, dim, vt, dev)
+        if shift is not None:
+            fp, fb = _vector("shift", shift, B, dim, vt, dev)
+        if gate is not None:
+            gp, gb = _vector("gate", gate, B, dim, vt, dev)
     if out is None:
-        out = _allocate(stream, torch.empty, shape, dtype=bf16, device=dev)
-    if y is not None and x_out is None:
-        x_out = _allocate(stream, torch.empty, shape, dtype=x.dtype, device=dev)
+        out = _allocate(stream, torch.empty, shape, dtype=bf16, device=x.device)
     hp, hb, hr = _token_rows("out", out, shape, bf16, dev)
-    yp, yb, yr = _token_rows("y", y, shape, bf16, dev) if y is not None else (None, 0, 0)
-    op, ob, orow = (_token_rows("x_out", x_out, shape, x.dtype, dev) if y is not None
-                    else (None, 0, 0))
-    rc = lib.flux_modulated_norm(xp, xb, xr, int(x.dtype == torch.float32), yp, yb, yr, gp, gb, sp,
-                                 sb, fp, fb, vec_f32, B, S, dim, NORMS[norm], float(eps), op, ob,
-                                 orow, hp, hb, hr, handle)
+    if y is not None:
+        yp, yb, yr = _token_rows("y", y, shape, bf16, dev)
+        if x_out is None:
+            x_out = _allocate(stream, torch.empty, shape, dtype=dtype, device=x.device)
+        op, ob, orow = _token_rows("x_out", x_out, shape, dtype, dev)
+    elif gate is not None or x_out is not None:
+        raise ValueError("gate and x_out need y")
+    rc = lib.flux_modulated_norm(xp, xb, xr, int(dtype != bf16), yp, yb, yr, gp, gb, sp, sb, fp,
+                                 fb, vec_f32, B, S, dim, kind, float(eps), op, ob, orow, hp, hb,
+                                 hr, handle)
     if rc != 0:
         raise FluxError("flux_modulated_norm", rc, lib)
     return out if y is None else (out, x_out)

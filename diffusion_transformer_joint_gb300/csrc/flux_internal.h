@@ -150,10 +150,10 @@ struct LinearProblem {
 struct LinearEpilogue;
 
 // How linear_split runs a problem: token rows as P (else W rows), the 256 x Q
-// tile, the CTA pairs that split its channels, the ring; how linear_pair does:
-// the tile's width. Both with an estimate of the time in ns.
+// tile, the CTA pairs that split its channels, the ring, whether sums arrive
+// early; how linear_pair does: the tile's width. Both with an estimate of the time in ns.
 struct SplitPlan {
-  bool tokens_p;
+  bool tokens_p, early;
   int Q, C, stages;
   double ns;
 };

@@ -178,16 +178,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;          // stage
     uint32_t turn = 0;  // times round the ring
     bool ok = true;
+    // the even CTA's W rows: the tile's first half, or its gate features; the
+    // odd CTA's: the second half, or the linear features
+    auto w_row = [&](int ft) {
+      const int64_t f0 = static_cast<int64_t>(ft) * feats;
+      return static_cast<int>(crank == 0 ? f0 : kGlu ? p.N + f0 : f0 + p.tn / 2);
+    };
     grid_dep_wait();
     for (int t = cid; ok && t < p.n_tiles; t += ncl) {
       int ft, rb;
       tile_at(p, t, ft, rb);
       const int b = rb / p.n_sb;
       const int s0 = (rb - b * p.n_sb) * (2 * kRows) + static_cast<int>(crank) * kRows;
-      // the even CTA's W rows: the tile's first half, or its gate features;
-      // the odd CTA's: the second half, or the linear features
-      const int64_t f0 = static_cast<int64_t>(ft) * feats;
-      const int rw = static_cast<int>(crank == 0 ? f0 : kGlu ? p.N + f0 : f0 + p.tn / 2);
+      const int rw = w_row(ft);
       for (int ks = 0; ks < p.nk; ++ks) {
         if (!(ok = mbar_wait_cluster(bar(kBarEmpty + s), (turn & 1u) ^ 1u, abort_flag))) break;
         const uint32_t dst = sbase + s * stage_bytes;

@@ -14,9 +14,8 @@
 // are no help: an SM takes in about 104 GB/s, and a stage of 64 channels brings
 // 128 bytes for each of its 128 + Q / 2 rows whatever the tile computes with
 // them. So the channels of a tile are split over C = 1 to 4 pairs of a
-// cluster: each CTA writes its fp32 partial sums to its shared memory, and
-// after a cluster barrier sends every other pair that pair's share of the
-// tokens (bulk copies between the CTAs' shared memories); each then adds the
+// cluster: each CTA writes its fp32 partial sums to its shared memory and
+// sends every other pair that pair's share of the tokens (bulk copies between the CTAs' shared memories); each then adds the
 // partials of its own share in the pairs' order (the same in every run) and
 // writes the finished rows. No workspace, no atomics, one launch. (Read by the
 // adding CTA with loads from distributed shared memory, about 24 bytes per ns
@@ -49,6 +48,7 @@ constexpr int kThreads = 512;
 constexpr uint32_t kSmemAll = 232448;   // one CTA per SM
 constexpr uint32_t kSmemHalf = 114688;  // two CTAs per SM
 constexpr uint32_t kTailBytes = 256;    // barriers and flags
+constexpr uint32_t kEarlyRing = 176 * 1024;
 
 struct SplitShape {
   int64_t N, o_bs, o_rs, r_bs, r_rs;
@@ -61,6 +61,7 @@ struct SplitShape {
   int feats;       // output features per tile (of a CTA, with W as P)
   int nk1, nk;     // stages of x, in all
   int stages, tmem_cols;
+  int early;       // sums have a place of their own to arrive at
   uint32_t pitch;  // bytes per token of the partial sums
   uint32_t recv;   // where the other pairs' partial sums arrive
   uint32_t tail;   // barriers, behind the stages and the sums
@@ -145,15 +146,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_sync_all();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // everything up to here overlaps the end of the kernel before this one
   grid_dep_launch_dependents();
+  // first rows of this CTA's share of W
+  const int w0 =
+      static_cast<int>(kTokensP ? (side == 0 ? f0 : kGlu ? p.N + f0 : f0 + p.Q / 2) : f0);
+  // everything up to here overlaps the end of the kernel before this one
   grid_dep_wait();
 
   if (warp == 0 && lane == 0) {
     const uint32_t bytes = kPBytes + static_cast<uint32_t>(p.q_rows) * kRowBytes;
-    // first rows of this CTA's share of W
-    const int w0 = static_cast<int>(
-        kTokensP ? (side == 0 ? f0 : kGlu ? p.N + f0 : f0 + p.Q / 2) : f0);
     const int x0 = kTokensP ? s0 : side * p.Sh;
     bool ok = true;
     int s = 0;
@@ -265,12 +266,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   fence_proxy_async_smem();
   tc_fence_before_sync();
-  __syncwarp();
-  cluster_sync_all();
-  if (warp == 2) {
-    tc_fence_after_sync();
-    tmem_dealloc_pair(tmem, static_cast<uint32_t>(p.tmem_cols));
-  }
+  // where sums arrive over the ring, every CTA of the cluster is done with its
+  if (kC > 1 && !p.early)
+    cluster_sync_all();
+  else
+    __syncthreads();
   // A thread finishes four features of tokens `per` apart. The loop is short
   // and its latencies are left to the 16 warps: this code runs once, and
   // unrolled it cost more in instruction misses than it saved.
@@ -284,6 +284,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     bias = load_vec4(epi.bias, f, epi.vec_f32);
     if constexpr (kGlu) bias_u = load_vec4(epi.bias, p.N + f, epi.vec_f32);
   }
+  // the first token's residual and gate come while the sums arrive
+  float4 gate = bias;
+  uint32_t gate_row = 0xFFFFFFFFu;  // of `gate`
+  // (at most 2^30 tokens: 32 bits do)
+  auto load_gate = [&](int b, int s) {
+    const uint32_t row =
+        static_cast<uint32_t>(b * p.S + s) / static_cast<uint32_t>(epi.gate_rows);
+    if (row != gate_row) gate = load_vec4(epi.gate, row * epi.gate_bs + f, epi.vec_f32);
+    gate_row = row;
+  };
+  int r = row_lo + tid / n_quad;
+  int b, s;
+  bool in = mine && r < row_hi && token_of(r, b, s);
+  uint2 res;
+  if (in && residual != nullptr)
+    res = *reinterpret_cast<const uint2 *>(residual + b * p.r_bs + s * p.r_rs + f);
+  if (in && epi.gate != nullptr) load_gate(b, s);
   // where row row_lo of every pair's partial sums lies: this one's own, or
   // where the others' arrive
   uint32_t sums[kC];
@@ -312,14 +329,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (mine) {
     const uint32_t half = static_cast<uint32_t>(p.feats) * 4;  // SwiGLU: to the linear sums
-    float4 gate = bias;
-    uint32_t gate_row = 0xFFFFFFFFu;  // of `gate`
-    int r = row_lo + tid / n_quad;
-    int b, s;
-    bool in = r < row_hi && token_of(r, b, s);
-    uint2 res;
-    if (in && residual != nullptr)
-      res = *reinterpret_cast<const uint2 *>(residual + b * p.r_bs + s * p.r_rs + f);
 #pragma unroll 1
     for (; r < row_hi; r += per) {
       // the next row's residual is on its way while this one is finished
@@ -344,11 +353,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           y = make_float4(activate<kAct>(y.x), activate<kAct>(y.y), activate<kAct>(y.z),
                           activate<kAct>(y.w));
         if (epi.gate != nullptr) {
-          // (at most 2^30 tokens: 32 bits do)
-          const uint32_t row = static_cast<uint32_t>(b * p.S + s) /
-                               static_cast<uint32_t>(epi.gate_rows);
-          if (row != gate_row) gate = load_vec4(epi.gate, row * epi.gate_bs + f, epi.vec_f32);
-          gate_row = row;
+          load_gate(b, s);
           y.x *= gate.x, y.y *= gate.y, y.z *= gate.z, y.w *= gate.w;
         }
         if (residual != nullptr)
@@ -362,14 +367,21 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncwarp();
   cluster_wait();  // what this CTA sent has arrived: its shared memory may go
+  if (warp == 2) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, static_cast<uint32_t>(p.tmem_cols));
+  }
   if (tid == 0 && *abort_flag) atomicExch(status, FLUX_ERR_DEVICE_TIMEOUT);
 }
 
-// Shared memory of a CTA's partial sums and those that arrive for it.
-uint32_t sums_bytes(bool tokens_p, int Q, int C) {
+// Shared memory of the partial sums of a CTA's rows; of those that arrive.
+uint32_t own_bytes(bool tokens_p, int Q) {
+  return static_cast<uint32_t>(tokens_p ? kP * (Q * 4 + 16) : Q * kP * 4);
+}
+uint32_t recv_bytes(bool tokens_p, int Q, int C) {
   const uint32_t rows = static_cast<uint32_t>(tokens_p ? kP : Q);
   const uint32_t pitch = static_cast<uint32_t>(tokens_p ? Q * 4 + 16 : kP * 4);
-  return (rows + static_cast<uint32_t>(C - 1) * ((rows + C - 1) / C)) * pitch;
+  return static_cast<uint32_t>(C - 1) * ((rows + C - 1) / C) * pitch;
 }
 
 template <int kAct, bool kTokensP, int kC>
@@ -410,8 +422,12 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
   p.pitch = static_cast<uint32_t>(kTokensP ? p.Q * 4 + 16 : kP * 4);
   p.stages = plan.stages;
   const uint32_t stage = kPBytes + static_cast<uint32_t>(p.Q / 2) * kRowBytes;
-  p.recv = static_cast<uint32_t>(kTokensP ? kP : p.Q) * p.pitch;
-  p.tail = std::max(static_cast<uint32_t>(p.stages) * stage, sums_bytes(kTokensP, p.Q, kC));
+  // the CTA's own partial sums over the drained ring, the others' behind them
+  const uint32_t ring = static_cast<uint32_t>(p.stages) * stage;
+  const uint32_t own = own_bytes(kTokensP, p.Q);
+  p.early = plan.early ? 1 : 0;
+  p.recv = plan.early ? std::max(ring, own) : own;
+  p.tail = std::max(ring, p.recv + recv_bytes(kTokensP, p.Q, kC));
   const uint32_t smem = p.tail + kTailBytes;
   if (smem > kSmemAll) return cudaErrorInvalidValue;
   const uint32_t w_box = static_cast<uint32_t>(kTokensP ? p.Q / 2 : p.feats);
@@ -481,7 +497,7 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
                               static_cast<double>(q.B * q.S) * q.N *
                                   (q.residual != nullptr ? 2 : 1));
   static constexpr int kWhole[kMaxC] = {152, 144, 138, 120}, kHalf[kMaxC] = {304, 296, 276, 288};
-  SplitPlan best{false, 32, 1, 2, 1e30};
+  SplitPlan best{false, false, 32, 1, 2, 1e30};
   auto consider = [&](bool tokens_p, int Q) {
     const int64_t feats = (tokens_p ? Q : 2 * kP) / (glu ? 2 : 1);  // of a tile
     const int64_t tiles =
@@ -491,13 +507,18 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
     const int cta_feats = (tokens_p ? Q : kP) / (glu ? 2 : 1);
     const double pitch = tokens_p ? Q * 4 + 16 : kP * 4;
     for (int C = 1; C <= kMaxC && C <= nk; ++C) {
-      const uint32_t sums = sums_bytes(tokens_p, Q, C);
+      const uint32_t recv = recv_bytes(tokens_p, Q, C);
       const int64_t ctas = tiles * 2 * C;
       const int64_t whole = kWhole[C - 1] * static_cast<int64_t>(sms) / 152;
       for (int half = 0; half < 2; ++half) {
         const uint32_t room = (half ? kSmemHalf : kSmemAll) - kTailBytes;
-        const int stages = static_cast<int>(std::min<uint32_t>(kMaxStages, room / stage));
-        if (sums > room || stages < 3) continue;
+        if (own_bytes(tokens_p, Q) + recv > room || 3 * stage > room) continue;
+        int stages = static_cast<int>(std::min<uint32_t>(kMaxStages, room / stage));
+        // a place of their own for the sums saves a cluster barrier, unless the
+        // ring gets short for it
+        const bool early = recv + kEarlyRing <= room;
+        if (early)
+          stages = static_cast<int>(std::min<uint32_t>(kMaxStages, (room - recv) / stage));
         const int64_t slots = half ? kHalf[C - 1] * static_cast<int64_t>(sms) / 152 : whole;
         const double waves = static_cast<double>((ctas + slots - 1) / slots);
         const double shared = !half ? 1.0 : std::min(ctas, slots) > sms ? 2.0 : ctas > whole ? 1.4 : 1.0;
@@ -508,13 +529,14 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
             waves * 2130.0 + 2100.0 - (half && ctas <= whole ? 260.0 : 0.0) +
             (C > 1 ? 520.0 + (C - 1) * (rows / static_cast<double>(C)) * pitch / 65.0 : 0.0) +
             0.17 * rows / C * cta_feats;
-        if (ns < best.ns) best = SplitPlan{tokens_p, Q, C, stages, ns};
+        if (ns < best.ns) best = SplitPlan{tokens_p, early, Q, C, stages, ns};
       }
     }
   };
   const int64_t rows_q = q.B * ((q.S + 15) / 16 * 16);
   if (rows_q <= 256) consider(false, static_cast<int>((rows_q + 31) / 32 * 32));
-  for (int Q = 32; Q <= 256; Q += 32) consider(true, Q);
+  if (q.B * q.S >= 64)  // fewer tokens would fill less than a quarter of P
+    for (int Q = 32; Q <= 256; Q += 32) consider(true, Q);
   return best;
 }
 

@@ -151,15 +151,15 @@ __device__ __forceinline__ Kept<kF32> get_kept(const void *base, int64_t off, bo
   const char *at = static_cast<const char *>(base) + off * (kF32 ? 4 : 2);
   const int step = (hi_in ? kHalfStep<kQuad> : 0) * (kF32 ? 4 : 2);
   if constexpr (kF32) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(at));
-    const uint4 b = __ldg(reinterpret_cast<const uint4 *>(at + step));
+    const uint4 a = *reinterpret_cast<const uint4 *>(at);
+    const uint4 b = *reinterpret_cast<const uint4 *>(at + step);
     return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
   } else if constexpr (kQuad) {
-    const uint2 a = __ldg(reinterpret_cast<const uint2 *>(at));
-    const uint2 b = __ldg(reinterpret_cast<const uint2 *>(at + step));
+    const uint2 a = *reinterpret_cast<const uint2 *>(at);
+    const uint2 b = *reinterpret_cast<const uint2 *>(at + step);
     return {{a.x, a.y, b.x, b.y}};
   } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(at));
+    const uint4 a = *reinterpret_cast<const uint4 *>(at);
     return {{a.x, a.y, a.z, a.w}};
   }
 }
@@ -318,6 +318,9 @@ __global__ void __launch_bounds__(kBlockWarps<kVec, kY, kVecF32> * 32, 1)
     }
     copy_async_commit();
   };
+  // everything up to here overlaps the end of the kernel before this one
+  grid_dep_launch_dependents();
+  grid_dep_wait();
   const uint32_t slots_end = slots + static_cast<uint32_t>(p.depth) * kSlot;
   for (uint32_t slot = slots; slot < slots_end; slot += kSlot) fetch(slot);
 
@@ -444,8 +447,17 @@ cudaError_t launch(const ModulatedNorm &q, int W, int sms, cudaStream_t stream) 
                                                static_cast<int>(kRing));
     if (e != cudaSuccess) return e;
   }
-  kernel<<<static_cast<unsigned>(blocks), p.groups * W * 32, smem, stream>>>(q, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(p.groups * W * 32), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, q, p);
 }
 
 template <int kVec>

@@ -134,13 +134,13 @@ def test_binding_refuses_cpu_tensors(lib):
 
 def test_vector_helper_shapes():
     v = torch.zeros(3, 16)
-    assert binding._vector("gate", v, 3, 16, v.dtype, v.device)[1] == 16
-    assert binding._vector("gate", v[0], 3, 16, v.dtype, v.device)[1] == 0
-    assert binding._vector("gate", v[:1], 3, 16, v.dtype, v.device)[1] == 0
-    assert binding._vector("gate", v[0].expand(3, 16), 3, 16, v.dtype, v.device)[1] == 0
+    assert binding._vector("gate", v, 3, 16, v.dtype, -1)[1] == 16
+    assert binding._vector("gate", v[0], 3, 16, v.dtype, -1)[1] == 0
+    assert binding._vector("gate", v[:1], 3, 16, v.dtype, -1)[1] == 0
+    assert binding._vector("gate", v[0].expand(3, 16), 3, 16, v.dtype, -1)[1] == 0
     for bad in (v[:2], v[:, :8], v.T, v[None], v[:, ::2]):
         with pytest.raises(ValueError):
-            binding._vector("gate", bad, 3, 16, v.dtype, v.device)
+            binding._vector("gate", bad, 3, 16, v.dtype, -1)
     with pytest.raises(ValueError, match="one type"):
         binding._vector_type(("bias", "gate"), (v, v.bfloat16()))
     with pytest.raises(ValueError, match="bfloat16 or float32"):

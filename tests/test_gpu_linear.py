@@ -256,3 +256,33 @@ def test_refusals():
         binding.linear(**dict(ops, x=ops["x"], w=ops["w"][:64], bias=None, gate=None,
                               residual=None), out=ops["x"])
     assert e.value.status == -9
+
+
+def _draws(n):
+    """Problems over the kernels' forms: tiles of W or of token rows, widths,
+    splits of the channels, both sides of their borders."""
+    import random
+
+    rng = random.Random(11)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))  # noqa: E731
+    for i in range(n):
+        K = 8 * log(1, 700)
+        yield (rng.choice((1, 1, 2, 3)), log(1, 900), K, 8 * log(1, 260),
+               dict(K2=rng.choice((0, 0, 8 * log(1, 200))),
+                    act=rng.choice((None, "silu", "gelu_tanh", "swiglu")),
+                    bias=rng.random() < 0.5, gate=rng.random() < 0.6,
+                    residual=rng.random() < 0.6,
+                    vec=rng.choice((torch.bfloat16, torch.float32)), seed=i),
+               rng.random() < 0.4)
+
+
+@pytest.mark.parametrize("B,S,K,N,kw,strided", list(_draws(60)))
+def test_drawn_problems(B, S, K, N, kw, strided):
+    ops = _make(B, S, K, N, **kw)
+    if strided:  # trailing tokens of longer buffers: batch elements cannot be joined
+        for name in ("x", "x2", "residual"):
+            if ops[name] is not None:
+                ops[name] = torch.cat([torch.full_like(ops[name][:, :1], float("nan")),
+                                       ops[name]], 1)[:, 1:]
+    out = torch.full((B, S + 2, N), 7.0, dtype=torch.bfloat16, device="cuda")[:, 1:-1]
+    R.check(_run(ops, out=out), R.linear(**ops), f"{B}x{S}x{K}->{N}")
