@@ -649,31 +649,33 @@ def _vector(name, t, B, width, dtype, dev):
     """(address, batch stride) of a vector [width], or of one per batch element
     [B, width] (a stride of 0 where all are the same)."""
     shape, st = t.shape, t.stride()
-    if shape[-1:] != (width,) or len(shape) > 2 or (len(shape) == 2 and shape[0] not in (1, B)):
+    n = len(shape)
+    if n == 2:
+        bs = st[0] if shape[0] == B and B > 1 else 0
+        if shape[0] not in (1, B) or shape[1] != width:
+            n = 0
+    elif n != 1 or shape[0] != width:
+        n = 0
+    if n == 0:
         raise ValueError(f"{name} must be [{width}] or [{B}, {width}], got {tuple(shape)}")
     if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} must be {dtype} like the other vectors, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
-    if width > 1 and st[-1] != 1:
+    if st[-1] != 1 and width > 1:
         raise ValueError(f"{name} must be contiguous, got strides {st}")
-    return t.data_ptr(), (st[0] if len(shape) == 2 and shape[0] == B and B > 1 else 0)
+    return t.data_ptr(), bs if n == 2 else 0
 
 
-def _vector_type(names, vecs):
-    """The one type of the vectors given: (dtype, vec_f32)."""
+def _vector_type(dtype):
+    """vec_f32 of a call whose vectors have this type."""
     import torch
 
-    dtype = None
-    for name, t in zip(names, vecs):
-        if t is None:
-            continue
-        if t.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError(f"{', '.join(names)} must have one type")
-        dtype = t.dtype
-    return dtype, int(dtype == torch.float32)
+    if dtype == torch.bfloat16:
+        return 0
+    if dtype != torch.float32:
+        raise ValueError(f"bias, gate, scale and shift must be bfloat16 or float32, got {dtype}")
+    return 1
 
 
 def _stream_of(x, stream):
@@ -745,7 +747,8 @@ def linear(x, w, x2=None, bias=None, act=None, gate=None, residual=None, out=Non
     if residual is not None:
         rp, rb, rr = _token_rows("residual", residual, shape, bf16, dev)
     if bias is not None or gate is not None:
-        vt, vec_f32 = _vector_type(("bias", "gate"), (bias, gate))
+        vt = (bias if bias is not None else gate).dtype
+        vec_f32 = _vector_type(vt)
         if bias is not None:
             bp = _vector("bias", bias, 1, rows, vt, dev)[0]
         if gate is not None:
@@ -792,7 +795,8 @@ def modulated_norm(x, scale=None, shift=None, y=None, gate=None, norm="layer", e
     sp = fp = gp = yp = op = None
     sb = fb = gb = yb = yr = ob = orow = vec_f32 = 0
     if scale is not None or shift is not None or gate is not None:
-        vt, vec_f32 = _vector_type(("scale", "shift", "gate"), (scale, shift, gate))
+        vt = (scale if scale is not None else shift if shift is not None else gate).dtype
+        vec_f32 = _vector_type(vt)
         if scale is not None:
             sp, sb = _vector("scale", scale, B, dim, vt, dev)
         if shift is not None:

@@ -157,9 +157,12 @@ int flux_linear(const void *x, int64_t x_bs, int64_t x_rs, int K, const void *x2
     q.B = 1;
     q.S = B * S;
   }
+  // the form with the smaller estimate; with few tokens most rows of linear_pair's
+  // tiles would be empty, and its estimate is not fitted there
   const int sms = flux::sm_count_current_device();
   const flux::SplitPlan split = flux::plan_split(q, act, sms);
-  const flux::PairPlan pair = flux::plan_pair(q, act, sms);
+  flux::PairPlan pair{0, 2e30};
+  if (q.B * q.S >= 128) pair = flux::plan_pair(q, act, sms);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = split.ns < pair.ns
                             ? flux::launch_linear_split(q, split, epi, act, status, st)

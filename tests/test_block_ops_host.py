@@ -141,10 +141,11 @@ def test_vector_helper_shapes():
     for bad in (v[:2], v[:, :8], v.T, v[None], v[:, ::2]):
         with pytest.raises(ValueError):
             binding._vector("gate", bad, 3, 16, v.dtype, -1)
-    with pytest.raises(ValueError, match="one type"):
-        binding._vector_type(("bias", "gate"), (v, v.bfloat16()))
+    with pytest.raises(ValueError, match="like the other vectors"):
+        binding._vector("gate", v, 3, 16, torch.bfloat16, -1)
     with pytest.raises(ValueError, match="bfloat16 or float32"):
-        binding._vector_type(("bias", "gate"), (v.double(), None))
+        binding._vector_type(torch.float64)
+    assert binding._vector_type(torch.float32) == 1 and binding._vector_type(torch.bfloat16) == 0
 
 
 def test_reference_linear_against_torch():
