@@ -26,11 +26,12 @@ void settle(Rows &t) {
   if (t.B == 1) t.bs = t.rs <= kMaxSpan / t.S ? t.S * t.rs : t.rs;
 }
 
-// Strides are positive multiples of 8 elements, and the rows fit the span.
+// Strides are multiples of 8 elements, no smaller than a row, and the rows fit
+// the span.
 bool strides_ok(const Rows &t) {
   if (t.rs <= 0 || t.bs <= 0 || t.rs % 8 != 0 || t.bs % 8 != 0) return false;
   if (t.rs > kMaxSpan / t.S || t.bs > kMaxSpan / t.B) return false;
-  return t.rs >= t.width || (t.S == 1);
+  return (t.S == 1 || t.rs >= t.width) && (t.B == 1 || t.bs >= t.width);
 }
 
 // No two rows of the tensor share an element (an output's condition): batch
@@ -153,9 +154,14 @@ int flux_linear(const void *x, int64_t x_bs, int64_t x_rs, int K, const void *x2
   const flux::LinearEpilogue epi{bias, gate, B > 1 ? gate_bs : 0, S, vec_f32};
   flux::LinearProblem q{x,     rx2.p, w,     residual, out,   rx.bs, rx.rs, rx2.bs, rx2.rs, rw.rs,
                         rr.bs, rr.rs, ro.bs, ro.rs,    B,     S,     N,     K,      K2};
-  if (B > 1 && joins(rx) && joins(rx2) && joins(rr) && joins(ro)) {
-    q.B = 1;
-    q.S = B * S;
+  if (S == 1) {  // batch elements of one token: tokens at the batch stride
+    q.x_rs = rx.bs, q.x2_rs = rx2.bs, q.r_rs = rr.bs, q.o_rs = ro.bs;
+    q.B = 1, q.S = B;
+  } else if (joins(rx) && joins(rx2) && joins(rr) && joins(ro)) {
+    q.B = 1, q.S = B * S;
+  }
+  if (q.B == 1) {  // (a batch stride that nothing looks at, but the tensor maps take)
+    q.x_bs = q.x_rs * q.S, q.x2_bs = q.x2_rs * q.S, q.r_bs = q.r_rs * q.S, q.o_bs = q.o_rs * q.S;
   }
   // the form with the smaller estimate; with few tokens most rows of linear_pair's
   // tiles would be empty, and its estimate is not fitted there

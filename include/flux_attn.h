@@ -397,8 +397,8 @@ int flux_qkv_mlp_proj(const void *x, const void *w, int64_t M, int dim, int H, i
  *
  * Strides. These entry points take token rows [B, S, width] whose channels are
  * contiguous, with a batch stride (_bs) and a token stride (_rs) in elements:
- * positive multiples of 8, the token stride at least the width (a stride whose
- * size is 1 is not looked at). So a stream may live inside a joint sequence
+ * multiples of 8, each at least the width (a stride whose size is 1 is not
+ * looked at). So a stream may live inside a joint sequence
  * or inside the columns of a wider buffer. An output's rows must not share
  * elements. Token pointers and vectors are 16-byte aligned. Vectors per batch
  * element (gate, scale, shift) have a batch stride that may be 0 (one vector

@@ -206,6 +206,64 @@ def test_on_another_stream_and_in_a_graph(S):
     assert int(status.item()) == 0
 
 
+@pytest.mark.parametrize("B", [1, 3, 40, 300])
+def test_one_token_of_every_batch_element(B):
+    """x[:, 4:5]-like views: the tokens lie a batch stride apart."""
+    ops = _make(B, 1, 136, 72, **FULL, act="silu", seed=B)
+    for name in ("x", "residual"):
+        buf = torch.full((B, 7, ops[name].shape[-1]), float("nan"), dtype=torch.bfloat16,
+                         device="cuda")
+        buf[:, 4:5] = ops[name]
+        ops[name] = buf[:, 4:5]
+    buf = torch.full((B, 5, 72), 7.0, dtype=torch.bfloat16, device="cuda")
+    R.check(_run(ops, out=buf[:, 2:3]), R.linear(**ops), "one token each")
+    buf[:, 2:3] = 7.0
+    assert bool((buf == 7.0).all())
+
+
+@pytest.mark.parametrize("S", [2, 500])
+def test_captured_behind_copies_and_across_streams(S):
+    """The kernels start under the end of the kernel before them: copies,
+    memsets, other streams' work and torch's kernels in front of them, and what
+    reads their output behind them, keep their order."""
+    ops = _make(1, S, 520, 136, **FULL, seed=S)
+    src = _make(1, S, 520, 136, **FULL, seed=S + 1)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, total = torch.empty_like(ops["residual"]), torch.empty_like(ops["residual"])
+
+    def steps():
+        side = torch.cuda.Stream()
+        ops["x"].copy_(src["x"])                      # a copy in front
+        binding.linear(**ops, out=out, status=status)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):                 # another stream reads, then writes
+            total.copy_(out)
+            binding.linear(src["x"], ops["w"], bias=src["bias"], out=total, status=status)
+        torch.cuda.current_stream().wait_stream(side)
+        out.zero_()                                   # a memset in front
+        binding.linear(**dict(ops, residual=total), out=out, status=status)
+        total.add_(out)                               # a torch kernel behind
+
+    steps()
+    torch.cuda.synchronize()
+    want = (out.clone(), total.clone())
+    part = binding.linear(src["x"], ops["w"], bias=src["bias"])
+    R.check(out, R.linear(src["x"], ops["w"], bias=ops["bias"], gate=ops["gate"], residual=part),
+            "after a copy")
+    assert torch.equal(total, part + out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps()
+    for _ in range(5):
+        out.fill_(float("nan"))
+        total.fill_(float("nan"))
+        ops["x"].fill_(float("nan"))
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(total, want[1])
+    assert int(status.item()) == 0
+
+
 def test_offsets_past_32_bits():
     """2.4e9 output elements, and a batch stride of as many: sampled rows."""
     S, K, N = 300_000, 64, 8192
