@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // then the odd CTA's
       const int hi = r >= p.Q / 2 ? 1 : 0;
       const int t = r - hi * (p.Q / 2);
-      b = t / p.Sh;
+      b = p.q_rows == p.Sh ? 0 : t / p.Sh;
       s = hi * p.Sh + t - b * p.Sh;
       return t < p.q_rows && s < p.S;
     }
@@ -287,10 +287,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   // the first token's residual and gate come while the sums arrive
   float4 gate = bias;
   uint32_t gate_row = 0xFFFFFFFFu;  // of `gate`
-  // (at most 2^30 tokens: 32 bits do)
   auto load_gate = [&](int b, int s) {
-    const uint32_t row =
-        static_cast<uint32_t>(b * p.S + s) / static_cast<uint32_t>(epi.gate_rows);
+    // joined batch elements (at most 2^30 tokens) are found by division
+    const uint32_t row = epi.gate_rows == p.S
+                             ? static_cast<uint32_t>(b)
+                             : static_cast<uint32_t>(s) / static_cast<uint32_t>(epi.gate_rows);
     if (row != gate_row) gate = load_vec4(epi.gate, row * epi.gate_bs + f, epi.vec_f32);
     gate_row = row;
   };
