@@ -166,6 +166,7 @@ int flux_linear(const void *x, int64_t x_bs, int64_t x_rs, int K, const void *x2
   // the form with the smaller estimate; with few tokens most rows of linear_pair's
   // tiles would be empty, and its estimate is not fitted there
   const int sms = flux::sm_count_current_device();
+  if (sms < 1) return FLUX_ERR_CUDA;
   const flux::SplitPlan split = flux::plan_split(q, act, sms);
   flux::PairPlan pair{0, 2e30};
   if (q.B * q.S >= 128) pair = flux::plan_pair(q, act, sms);

@@ -67,8 +67,8 @@ __device__ __forceinline__ float4 load_vec4(const void *base, int64_t off, int f
 }
 
 __device__ __forceinline__ float load_vec1(const void *base, int64_t off, int f32) {
-  return f32 ? static_cast<const float *>(base)[off]
-             : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(base)[off]) << 16);
+  if (f32) return static_cast<const float *>(base)[off];
+  return bf16lo_to_f32(static_cast<const uint16_t *>(base)[off]);
 }
 
 __device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {

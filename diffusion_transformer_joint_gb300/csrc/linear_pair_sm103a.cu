@@ -38,8 +38,8 @@
 //   and updated in place; lane 0 stores the box with one TMA copy. Rows past S
 //   and features past N are neither read nor written.
 // The two accumulators let the epilogue of one tile overlap the next tile's
-// MMAs; the last tile's is what a call pays for (with four warps, each reading
-// bias and gate from global memory, 10 us of the 83 that 4096 rows of 4096 -> 4096 channels took).
+// MMAs; the last tile's is what a call pays for (4 us with the residual; with
+// four warps, each reading bias and gate from global memory, it was 10 us).
 //
 // The launch overlaps its prologue with the end of the kernel before it in the
 // stream (programmatic dependent launch): what reads or writes global memory
@@ -72,7 +72,9 @@ constexpr int kBarAccFull = 2 * kMaxStages;
 constexpr int kBarAccEmpty = kBarAccFull + 2;  // (even CTA) both epilogues read it
 constexpr int kBarDrain = kBarAccEmpty + 2;
 constexpr int kBarRes = kBarDrain + 1;  // residual box landed, per warp and box
-constexpr int kNumBars = kBarRes + kEpiWarps * kBoxes;
+constexpr int kBarVecReady = kBarRes + kEpiWarps * kBoxes;  // a tile's vectors are staged
+constexpr int kBarVecFree = kBarVecReady + 1;               // every epilogue warp has read them
+constexpr int kNumBars = kBarVecFree + 1;
 constexpr uint32_t kOffBox = kRingBytes;
 constexpr uint32_t kOffVec = kOffBox + kEpiWarps * kBoxes * kBoxBytes;  // a tile's bias, gate
 constexpr uint32_t kOffBar = kOffVec + 2 * kMaxTn * 4;
@@ -109,13 +111,9 @@ __device__ __forceinline__ void bounded(uint32_t bar, uint32_t parity) {
   }
 }
 
-// The epilogue warps only.
-__device__ __forceinline__ void epi_barrier() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
-}
-
 __device__ __forceinline__ void read8(float (&v)[8], const float *p) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+  const float4 a = reinterpret_cast<const float4 *>(p)[0];
+  const float4 b = reinterpret_cast<const float4 *>(p)[1];
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
   v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
@@ -156,6 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(kBarDrain), 1);
     for (int i = 0; i < kEpiWarps * kBoxes; ++i) mbar_init(bar(kBarRes + i), 1);
+    mbar_init(bar(kBarVecReady), kEpiWarps);
+    mbar_init(bar(kBarVecFree), kEpiWarps);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bar_res = kBarRes + (warp - 4) * kBoxes;
     float *vec_bias = reinterpret_cast<float *>(base + kOffVec);
     float *vec_gate = vec_bias + kMaxTn;
-    uint32_t n_loaded = 0, n_stored = 0;  // boxes of this warp whose residual was asked for / staged
+    const bool vecs = epi.bias != nullptr || epi.gate != nullptr;
+    uint32_t n_loaded = 0, n_stored = 0;  // this warp's boxes: residual asked for, staged
     int lt = 0;
     bool ok = true;
     grid_dep_wait();
@@ -300,12 +301,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t gate_row = 0;
       if (epi.gate != nullptr) {
         const int64_t r0 = static_cast<int64_t>(b) * p.S + (sc < p.S ? sc : p.S - 1);
-        const int64_t r1 = static_cast<int64_t>(b) * p.S + (sc + kRows < p.S ? sc + kRows : p.S) - 1;
+        const int64_t r1 =
+            static_cast<int64_t>(b) * p.S + (sc + kRows < p.S ? sc + kRows : p.S) - 1;
         gate_row = r0 / epi.gate_rows;
         gate_rowwise = r1 / epi.gate_rows != gate_row;
       }
-      if (epi.bias != nullptr || epi.gate != nullptr) {
-        epi_barrier();
+      if (vecs) {
+        // (barriers with bounded waits: an aborting warp leaves the others)
+        if (lt > 0 && !(ok = __all_sync(0xffffffffu,
+                                        mbar_wait(bar(kBarVecFree),
+                                                  static_cast<uint32_t>(lt - 1) & 1u, abort_flag))))
+          break;
         if (epi.bias != nullptr && et < p.tn) {
           const int64_t f = f0 + (kGlu && et >= feats ? et - feats : et);
           if (f < p.N)
@@ -313,7 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (epi.gate != nullptr && !gate_rowwise && et < feats && f0 + et < p.N)
           vec_gate[et] = load_vec1(epi.gate, gate_row * epi.gate_bs + f0 + et, epi.vec_f32);
-        epi_barrier();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarVecReady));
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarVecReady),
+                                                     static_cast<uint32_t>(lt) & 1u, abort_flag))))
+          break;
       }
       if (gate_rowwise) {
         const int64_t r = static_cast<int64_t>(b) * p.S + (s0 + lane < p.S ? s0 + lane : p.S - 1);
@@ -398,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8u * static_cast<uint32_t>(lt & 1));
+      if (vecs && lane == 0) mbar_arrive(bar(kBarVecFree));
     }
     if (lane == 0) {
       // residual copies still in flight after an abort, then every output store

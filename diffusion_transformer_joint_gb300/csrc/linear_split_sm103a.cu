@@ -11,22 +11,21 @@
 // call, are read once. Otherwise P is token rows and Q features (kTokensP).
 //
 // Tiles alone are too few to draw the memory's bandwidth, and narrower ones
-// are no help: an SM takes in about 104 GB/s, and a stage of 64 channels brings
+// are no help: an SM takes in about 110 GB/s, and a stage of 64 channels brings
 // 128 bytes for each of its 128 + Q / 2 rows whatever the tile computes with
 // them. So the channels of a tile are split over C = 1 to 4 pairs of a
 // cluster: each CTA writes its fp32 partial sums to its shared memory and
-// sends every other pair that pair's share of the tokens (bulk copies between the CTAs' shared memories); each then adds the
+// sends every other pair that pair's share of the tokens (bulk copies between
+// the CTAs' shared memories, about 30 bytes per ns and SM); each then adds the
 // partials of its own share in the pairs' order (the same in every run) and
-// writes the finished rows. No workspace, no atomics, one launch. (Read by the
-// adding CTA with loads from distributed shared memory, about 24 bytes per ns
-// and SM, the partials of 512 x 4096 outputs took 5.4 us.)
+// writes the finished rows. No workspace, no atomics, one launch.
 //
 // For SwiGLU the W rows of a tile are the gate rows of its outputs and their
 // linear rows: side by side in each CTA as P, one CTA's each as Q.
 //
 // 16 warps: warp 0 TMA producer, warp 1 MMA issuer (in the pair's even CTA, one
-// M256 N=Q K16 MMA per 16 channels), warp 2 TMEM allocation; then all of
-// them move the CTA's 128 accumulator rows to shared memory over the drained stages
+// M256 N=Q K16 MMA per 16 channels), warp 2 TMEM allocation; then all of them
+// move the CTA's 128 accumulator rows to shared memory over the drained stages
 // and finish them. The prologue overlaps the end of the kernel before it
 // (programmatic dependent launch). Every wait is bounded; a wait that runs out
 // aborts the CTA and sets the status word to FLUX_ERR_DEVICE_TIMEOUT.
@@ -48,6 +47,8 @@ constexpr int kThreads = 512;
 constexpr uint32_t kSmemAll = 232448;   // one CTA per SM
 constexpr uint32_t kSmemHalf = 114688;  // two CTAs per SM
 constexpr uint32_t kTailBytes = 256;    // barriers and flags
+// A ring that sums may have a place of their own beside: with less on its way
+// than about 1.5 us of what an SM takes in, the stages wait for the memory.
 constexpr uint32_t kEarlyRing = 176 * 1024;
 
 struct SplitShape {
@@ -128,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_init(bar_acc, 1);
     mbar_init(bar_recv, 1);
     if (kC > 1)
-      mbar_arrive_expect_tx(bar_recv, static_cast<uint32_t>((kC - 1) * (row_hi - row_lo)) * p.pitch);
+      mbar_arrive_expect_tx(bar_recv,
+                            static_cast<uint32_t>((kC - 1) * (row_hi - row_lo)) * p.pitch);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -231,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       int b, s;
       const int r = i / lines;
       const int64_t f = f0 + (i - r * lines) * 64;
-      if (token_of(row_lo + r, b, s) && f < p.N) prefetch_l2(residual + b * p.r_bs + s * p.r_rs + f);
+      if (token_of(row_lo + r, b, s) && f < p.N)
+        prefetch_l2(residual + b * p.r_bs + s * p.r_rs + f);
     }
   }
   __syncwarp();
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // one TMEM lane, i.e. row of P, per thread; 16 rows of Q at a time
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t row = static_cast<uint32_t>((warp & 3) * 32 + lane);
-    #pragma unroll 1
+#pragma unroll 1
     for (int c = warp >> 2; c < p.Q / 16; c += kThreads / 128) {
       uint32_t r[16];
       tmem_ld16(tmem + lane_off + c * 16, r);
@@ -522,7 +525,8 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
           stages = static_cast<int>(std::min<uint32_t>(kMaxStages, (room - recv) / stage));
         const int64_t slots = half ? kHalf[C - 1] * static_cast<int64_t>(sms) / 152 : whole;
         const double waves = static_cast<double>((ctas + slots - 1) / slots);
-        const double shared = !half ? 1.0 : std::min(ctas, slots) > sms ? 2.0 : ctas > whole ? 1.4 : 1.0;
+        const double shared =
+            !half ? 1.0 : std::min(ctas, slots) > sms ? 2.0 : ctas > whole ? 1.4 : 1.0;
         const double per_stage =
             std::max(stage_ns(stage, Q) * shared, 1090.0 / static_cast<double>(stages));
         const double ns =

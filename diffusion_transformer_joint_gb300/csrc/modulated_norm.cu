@@ -28,11 +28,15 @@
 // on fp32 pairs. A thread holds 16 channels beside a residual's gate, else 32
 // (in a row of over 8192 channels with a residual 32 as well, and spills).
 //
+// The launch overlaps its prologue with the end of the kernel before it in the
+// stream (programmatic dependent launch); no tensor is touched before that
+// kernel has ended.
+//
 // Measured on a GB300, several inputs in turn: 4096 rows of 4096 channels bf16
-// 13.3 us, 5.0 TB/s (a kernel that only copies the rows takes 12.8); two times
-// 4608 rows of 4096 with an fp32 stream and the gated residual 71.9 us, 6.3
-// TB/s; 12800 rows of 6144 bf16 with the gated residual 93.6 us, 6.7 TB/s, as
-// fast as memory copies.
+// 12.9 us, 5.2 TB/s (a kernel that only copies the rows takes 12.8); two times
+// 4608 rows of 4096 with an fp32 stream and the gated residual 71.5 us, 6.3
+// TB/s; 12800 rows of 6144 bf16 with the gated residual 92.6 us, 6.8 TB/s, as
+// fast as memory copies; one row 2.1 us.
 #include <algorithm>
 
 #include "linear_common.cuh"
@@ -44,7 +48,7 @@ constexpr int kMaxGroupWarps = 16;
 constexpr uint32_t kRing = 200 * 1024;
 
 // Warps of a block, by the registers its threads need.
-template <int kVec, bool kY, bool kVecF32>
+template <int kVec, bool kY>
 constexpr int kBlockWarps = kVec <= 2 && !kY ? 24 : 16;
 
 // Rows that a block has in hand. Without a residual 16 or 24 warps' worth (four
@@ -231,13 +235,13 @@ __device__ __forceinline__ float group_sum(uint64_t v2, float4 *part, int W, int
 // kF32: type of x; kY: with the residual; kVecF32: type of the modulation;
 // kFull: dim = W * kVec * 256.
 template <int kVec, bool kF32, bool kY, bool kVecF32, bool kFull>
-__global__ void __launch_bounds__(kBlockWarps<kVec, kY, kVecF32> * 32, 1)
+__global__ void __launch_bounds__(kBlockWarps<kVec, kY> * 32, 1)
     modulated_norm_kernel(const ModulatedNorm q, const NormPlan p) {
   constexpr bool kQuad = kF32;
   constexpr int kXs = kF32 ? 4 : 2;  // bytes per channel
   constexpr int kSeg = kVec * 256;   // channels per warp
   constexpr uint32_t kXSeg = kSeg * kXs, kSlot = kXSeg + (kY ? kSeg * 2 : 0);
-  __shared__ float4 parts[kBlockWarps<kVec, kY, kVecF32>][3][kMaxGroupWarps / 4];
+  __shared__ float4 parts[kBlockWarps<kVec, kY>][3][kMaxGroupWarps / 4];
   extern __shared__ __align__(16) uint8_t ring[];
   const int W = p.W;
   const int lane = static_cast<int>(threadIdx.x & 31);
@@ -299,7 +303,8 @@ __global__ void __launch_bounds__(kBlockWarps<kVec, kY, kVecF32> * 32, 1)
       const uint32_t to = slot + lane * 16;
 #pragma unroll
       for (int j = 0; j < kVec * kXs / 2; ++j)
-        if (kFull || (j * 32 + lane) * (16 / kXs) < copy_left) copy_async_16(to + j * 512, xa + j * 512);
+        if (kFull || (j * 32 + lane) * (16 / kXs) < copy_left)
+          copy_async_16(to + j * 512, xa + j * 512);
       if constexpr (kY) {
 #pragma unroll
         for (int j = 0; j < kVec; ++j)
@@ -426,8 +431,9 @@ cudaError_t launch(const ModulatedNorm &q, int W, int sms, cudaStream_t stream) 
   p.rows = static_cast<int>(q.B * q.S);
   p.W = W;
   const uint32_t row = static_cast<uint32_t>(kVec * 256 * ((kF32 ? 4 : 2) + (kY ? 2 : 0)) * W);
+  const int warps = std::min(kBlockWarps<kVec, kY>, kRowWarps<kY>);
   p.groups = static_cast<int>(std::max<int64_t>(
-      1, std::min<int64_t>({std::min(kBlockWarps<kVec, kY, kVecF32>, kRowWarps<kY>) / W, kRing / (2 * row), (p.rows + sms - 1) / sms})));
+      1, std::min<int64_t>({warps / W, kRing / (2 * row), (p.rows + sms - 1) / sms})));
   const int blocks = std::min((p.rows + p.groups - 1) / p.groups, sms);
   p.step = blocks * p.groups;
   p.step_s = p.step % p.S;

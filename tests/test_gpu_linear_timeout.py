@@ -24,8 +24,10 @@ SPLIT = ("linear_split_sm103a.cu", "mma_commit_pair_elect(bar_empty(s), mask);",
          "if (turn != 0) mma_commit_pair_elect(bar_empty(s), mask);")
 
 
-@pytest.mark.parametrize("patch,S,K,N", [(PAIR, 2600, 64, 4096), (SPLIT, 9, 4096, 256)])
-def test_bounded_wait_reports_timeout_and_context_survives(tmp_path, patch, S, K, N):
+@pytest.mark.parametrize("patch,S,K,N,vecs", [(PAIR, 2600, 64, 4096, False),
+                                              (PAIR, 2600, 64, 4096, True),
+                                              (SPLIT, 9, 4096, 256, True)])
+def test_bounded_wait_reports_timeout_and_context_survives(tmp_path, patch, S, K, N, vecs):
     build.build()
     binding.load()
     name, anchor, withheld = patch
@@ -46,11 +48,14 @@ def test_bounded_wait_reports_timeout_and_context_survives(tmp_path, patch, S, K
     x = torch.randn(1, S, K, generator=g).bfloat16().cuda()
     w = (torch.randn(N, K, generator=g) * K ** -0.5).bfloat16().cuda()
     y = torch.zeros(1, S, N, dtype=torch.bfloat16, device="cuda")
+    bias = torch.randn(N, generator=g).bfloat16().cuda() if vecs else None
+    gate = torch.randn(N, generator=g).bfloat16().cuda() if vecs else None
+    P = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     torch.cuda.synchronize()
     t0 = time.time()
-    rc = lib.flux_linear(x.data_ptr(), 0, K, K, None, 0, 0, 0, w.data_ptr(), K, 1, S, N, 0, None,
-                         None, 0, 0, None, 0, 0, y.data_ptr(), 0, N, status.data_ptr(),
+    rc = lib.flux_linear(x.data_ptr(), 0, K, K, None, 0, 0, 0, w.data_ptr(), K, 1, S, N, 0, P(bias),
+                         P(gate), 0, 0, None, 0, 0, y.data_ptr(), 0, N, status.data_ptr(),
                          torch.cuda.current_stream().cuda_stream)
     assert rc == 0
     torch.cuda.synchronize()
@@ -58,8 +63,8 @@ def test_bounded_wait_reports_timeout_and_context_survives(tmp_path, patch, S, K
     assert int(status.item()) == -7, f"expected FLUX_ERR_DEVICE_TIMEOUT, got {int(status.item())}"
     assert elapsed < 60.0, f"bounded wait took {elapsed:.1f} s"
     status.zero_()
-    got = binding.linear(x, w, status=status)
+    got = binding.linear(x, w, bias=bias, gate=gate, status=status)
     torch.cuda.synchronize()
     assert int(status.item()) == 0
     rows = torch.tensor([0, S // 2, S - 1], device="cuda")
-    R.check(got[:, rows], R.linear(x[:, rows], w), "after the timeout")
+    R.check(got[:, rows], R.linear(x[:, rows], w, bias=bias, gate=gate), "after the timeout")
