@@ -149,11 +149,12 @@ struct LinearProblem {
 };
 struct LinearEpilogue;
 
-// How linear_split runs a problem: token rows as P (else W rows), the 256 x Q
-// tile, the CTA pairs that split its channels, the ring, whether sums arrive
-// early; how linear_pair does: the tile's width. Both with an estimate of the time in ns.
+// How linear_split runs a problem: its form, the tile's width, the units that
+// split its channels, whether their sums arrive early, the ring; how
+// linear_pair does: the tile's width. Both with an estimate of the time in ns.
 struct SplitPlan {
-  bool tokens_p, early;
+  int form;
+  bool early;
   int Q, C, stages;
   double ns;
 };

@@ -1,34 +1,43 @@
 // flux_linear where whole 256-row tiles would leave SMs idle (few rows, or few
-// features), on sm_103a (GB300): tiles of 256 rows of one operand against up
-// to 256 rows of the other, the channels split over a cluster.
+// features), on sm_103a (GB300): tiles of 128 or 256 rows of one operand
+// against up to 256 rows of the other, the channels split over a cluster.
 //
 //   out[b, s, :] = residual[b, s, :] + gate[b, :] * act([x | x2][b, s, :] W^T + bias)
 //
-// A tile is 256 x Q accumulators of a CTA pair: 256 rows of the operand P (128
-// per CTA, the MMA's M) against Q <= 256 rows of the operand Q (half of them in
-// each CTA's shared memory, the MMA's N). With few token rows P is W and Q
-// holds every token (kTokensP false), so that the weights, which bound such a
-// call, are read once. Otherwise P is token rows and Q features (kTokensP).
+// A unit is a CTA, or a CTA pair, that computes P x Q accumulators: 128 rows of
+// the operand P per CTA (the MMA's M) against Q <= 256 rows of the operand Q
+// (its N; in a pair each CTA's shared memory holds half of them). Three forms:
+//   kSingle  P is W, Q holds every token (64 at most), a unit is one CTA with
+//            half an SM's shared memory;
+//   kPairW   P is W, Q holds every token (256 at most), a unit is a pair;
+//   kPairX   P is token rows, Q features, a unit is a pair.
+// With W as P the weights, which bound a call with few tokens, are read once.
 //
 // Tiles alone are too few to draw the memory's bandwidth, and narrower ones
 // are no help: an SM takes in about 110 GB/s, and a stage of 64 channels brings
-// 128 bytes for each of its 128 + Q / 2 rows whatever the tile computes with
-// them. So the channels of a tile are split over C = 1 to 4 pairs of a
-// cluster: each CTA writes its fp32 partial sums to its shared memory and
-// sends every other pair that pair's share of the tokens (bulk copies between
-// the CTAs' shared memories, about 30 bytes per ns and SM); each then adds the
-// partials of its own share in the pairs' order (the same in every run) and
-// writes the finished rows. No workspace, no atomics, one launch.
+// 128 bytes for each of its rows whatever the tile computes with them. So the
+// channels of a tile are split over the units of a cluster (kC of them): each
+// CTA writes its fp32 partial sums to its shared memory and sends every other
+// unit that unit's share of the tokens (bulk copies between the CTAs' shared
+// memories, about 30 bytes per ns and SM); each then adds the partials of its
+// own share in the units' order (the same in every run) and writes the
+// finished rows. No workspace, no atomics, one launch.
 //
 // For SwiGLU the W rows of a tile are the gate rows of its outputs and their
 // linear rows: side by side in each CTA as P, one CTA's each as Q.
 //
-// 16 warps: warp 0 TMA producer, warp 1 MMA issuer (in the pair's even CTA, one
-// M256 N=Q K16 MMA per 16 channels), warp 2 TMEM allocation; then all of them
-// move the CTA's 128 accumulator rows to shared memory over the drained stages
-// and finish them. The prologue overlaps the end of the kernel before it
-// (programmatic dependent launch). Every wait is bounded; a wait that runs out
-// aborts the CTA and sets the status word to FLUX_ERR_DEVICE_TIMEOUT.
+// A CTA pair has its two SMs to itself. Two pairs on the same SMs would
+// allocate TMEM for both SMs at the same time, and an SM lets one CTA allocate
+// until that one is done: each pair could hold one SM and wait for the other
+// for ever. Two CTAs share an SM only where each allocates for itself.
+//
+// 16 warps: warp 0 TMA producer, warp 1 MMA issuer (of the pair's even CTA; one
+// K16 MMA per 16 channels), warp 2 TMEM allocation; then all of them move the
+// CTA's 128 accumulator rows to shared memory over the drained stages and
+// finish them. The prologue overlaps the end of the kernel before it
+// (programmatic dependent launch). Every wait on an mbarrier is bounded; a wait
+// that runs out aborts the CTA and sets the status word to
+// FLUX_ERR_DEVICE_TIMEOUT.
 #include <algorithm>
 #include <mutex>
 
@@ -42,10 +51,13 @@ constexpr int kK = 64;
 constexpr uint32_t kRowBytes = kK * 2;
 constexpr uint32_t kPBytes = kP * kRowBytes;
 constexpr int kMaxStages = 12;
-constexpr int kMaxC = 4;  // pairs that split a tile's channels
+constexpr int kSingle = 0, kPairW = 1, kPairX = 2;
+// units that split a tile's channels: clusters have up to eight CTAs
+constexpr int kMaxUnits = 8;
+constexpr int max_units(int form) { return form == kSingle ? kMaxUnits : kMaxUnits / 2; }
 constexpr int kThreads = 512;
-constexpr uint32_t kSmemAll = 232448;   // one CTA per SM
-constexpr uint32_t kSmemHalf = 114688;  // two CTAs per SM
+constexpr uint32_t kSmemAll = 232448;   // a pair's CTAs: one per SM
+constexpr uint32_t kSmemHalf = 114688;  // single CTAs: two per SM
 constexpr uint32_t kTailBytes = 256;    // barriers and flags
 // A ring that sums may have a place of their own beside: with less on its way
 // than about 1.5 us of what an SM takes in, the stages wait for the memory.
@@ -56,15 +68,15 @@ struct SplitShape {
   int S;           // tokens per batch element of the launch
   int Q;           // tile columns
   int q_rows;      // rows of Q that each CTA copies
-  int Sh;          // tokens as Q: half a batch element's tokens, rounded up to 8
+  int Sh;          // tokens as Q: a batch element's in one CTA, rounded up to 8
   int n_sb;        // tokens as P: 256-row blocks per batch element
   int n_ft;        // feature tiles
-  int feats;       // output features per tile (of a CTA, with W as P)
+  int feats;       // output features of a CTA's tile
   int nk1, nk;     // stages of x, in all
   int stages, tmem_cols;
   int early;       // sums have a place of their own to arrive at
   uint32_t pitch;  // bytes per token of the partial sums
-  uint32_t recv;   // where the other pairs' partial sums arrive
+  uint32_t recv;   // where the other units' partial sums arrive
   uint32_t tail;   // barriers, behind the stages and the sums
 };
 
@@ -82,15 +94,17 @@ __device__ __forceinline__ void add4(float4 &v, float4 a) {
   v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
 }
 
-template <int kAct, bool kTokensP, int kC>
+template <int kAct, int kForm, int kC>
 __global__ void __launch_bounds__(kThreads, 2)
     linear_split_kernel(const __grid_constant__ SplitMaps maps, const SplitShape p,
                         const LinearEpilogue epi, const uint16_t *residual, uint16_t *out,
                         int *status) {
   constexpr bool kGlu = kAct == FLUX_ACT_SWIGLU;
+  constexpr bool kPair = kForm != kSingle, kTokensP = kForm == kPairX;
   extern __shared__ __align__(1024) uint8_t base[];
   const uint32_t sbase = smem_addr(base);
-  const uint32_t stage_bytes = kPBytes + static_cast<uint32_t>(p.Q / 2) * kRowBytes;
+  const int q_cta = kPair ? p.Q / 2 : p.Q;  // rows of Q in this CTA
+  const uint32_t stage_bytes = kPBytes + static_cast<uint32_t>(q_cta) * kRowBytes;
   const uint32_t tail = p.tail;
   auto bar_full = [&](int s) { return sbase + tail + 16u * static_cast<uint32_t>(s); };
   auto bar_empty = [&](int s) { return sbase + tail + 16u * static_cast<uint32_t>(s) + 8u; };
@@ -102,22 +116,25 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int warp = tid >> 5;
   const int lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
-  const uint32_t even = rank & ~1u;            // the pair's even CTA: issues its MMAs
-  const int side = static_cast<int>(rank & 1u);
-  const int part = static_cast<int>(rank >> 1);  // of the channels
+  const uint32_t even = kPair ? rank & ~1u : rank;  // the CTA that issues the unit's MMAs
+  const int side = static_cast<int>(rank - even);
+  const int part = static_cast<int>(kPair ? rank >> 1 : rank);  // of the channels
+  auto rank_of = [&](int unit) {  // the CTA with this one's rows of P in another unit
+    return static_cast<uint32_t>(kPair ? 2 * unit + side : unit);
+  };
   // the tile: its first feature, and with tokens as P its batch element and
   // this CTA's first token
   const int tile = static_cast<int>(cluster_id_x());
   const int tb = tile / p.n_ft;
   const int ft = tile - tb * p.n_ft;
-  const int64_t f0 = static_cast<int64_t>(kTokensP ? ft : 2 * ft + side) * p.feats;
+  const int64_t f0 = static_cast<int64_t>(kForm == kPairW ? 2 * ft + side : ft) * p.feats;
   const int b0 = kTokensP ? tb / p.n_sb : 0;
   const int s0 = kTokensP ? ((tb - b0 * p.n_sb) * 2 + side) * kP : 0;
   // the tokens (rows of the partial sums) that this CTA finishes
   const int n_rows = kTokensP ? kP : p.Q;
   auto row_of = [&](int r) { return n_rows * r / kC; };
   const int row_lo = row_of(part), row_hi = row_of(part + 1);
-  // the pair's channels: an even share of the stages (at least one: kC <= nk)
+  // the unit's channels: an even share of the stages (at least one: kC <= nk)
   const int k_lo = static_cast<int>(static_cast<int64_t>(p.nk) * part / kC);
   const int k_hi = static_cast<int>(static_cast<int64_t>(p.nk) * (part + 1) / kC);
 
@@ -135,14 +152,19 @@ __global__ void __launch_bounds__(kThreads, 2)
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc_pair(smem_addr(tmem_slot), static_cast<uint32_t>(p.tmem_cols));
-    tmem_relinquish_pair();
+    if constexpr (kPair) {
+      tmem_alloc_pair(smem_addr(tmem_slot), static_cast<uint32_t>(p.tmem_cols));
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_addr(tmem_slot), static_cast<uint32_t>(p.tmem_cols));
+      tmem_relinquish();
+    }
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&maps.x);
     tma_prefetch_desc(&maps.w);
   }
-  // both CTAs' barriers are initialised before either signals the other's
+  // every CTA's barriers are initialised before another signals them
   tc_fence_before_sync();
   __syncwarp();
   cluster_sync_all();
@@ -166,19 +188,25 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t dst = sbase + static_cast<uint32_t>(s) * stage_bytes;
       const uint32_t dst_w = kTokensP ? dst + kPBytes : dst;
       const uint32_t dst_x = kTokensP ? dst : dst + kPBytes;
-      // both CTAs' copies complete on the even CTA's stage barrier
-      if (side == 0) mbar_arrive_expect_tx(bar_full(s), 2 * bytes);
-      const uint32_t full = mapa_shared(bar_full(s), even);
+      // the unit's copies complete on its even CTA's stage barrier
+      if (side == 0) mbar_arrive_expect_tx(bar_full(s), (kPair ? 2 : 1) * bytes);
+      const uint32_t full = kPair ? mapa_shared(bar_full(s), even) : bar_full(s);
+      auto load = [&](uint32_t to, const void *map, int c0, int c1, int c2) {
+        if constexpr (kPair)
+          tma_load_3d_pair(to, map, full, c0, c1, c2);
+        else
+          tma_load_3d(to, map, full, c0, c1, c2);
+      };
       const bool first = ks < p.nk1;
       const int c = (first ? ks : ks - p.nk1) * kK;
       const void *wm = first ? &maps.w : &maps.w2;
-      tma_load_3d_pair(dst_w, wm, full, c, w0, 0);
+      load(dst_w, wm, c, w0, 0);
       if constexpr (kGlu && !kTokensP)
-        tma_load_3d_pair(dst_w + kPBytes / 2, wm, full, c, static_cast<int>(p.N) + w0, 0);
-      tma_load_3d_pair(dst_x, first ? &maps.x : &maps.x2, full, c, x0, b0);
+        load(dst_w + kPBytes / 2, wm, c, static_cast<int>(p.N) + w0, 0);
+      load(dst_x, first ? &maps.x : &maps.x2, c, x0, b0);
       if (++s == p.stages) s = 0, ++turn;
     }
-    // every copy of the pair has landed before the CTAs exit (the final cluster
+    // every copy of the unit has landed before its CTAs exit (the final cluster
     // barrier keeps the odd CTA until then)
     if (side == 0)
       for (int i = 0; i < p.stages; ++i) {
@@ -189,8 +217,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           bounded(bar_full(i), (turn - 1) & 1u);
       }
   } else if (warp == 1 && side == 0) {
-    const uint32_t idesc = idesc_bf16_f32(2 * kP, p.Q, 0, 0);
-    const uint16_t mask = static_cast<uint16_t>(0x3u << even);
+    const uint32_t idesc = idesc_bf16_f32(kPair ? 2 * kP : kP, p.Q, 0, 0);
+    auto commit = [&](uint32_t bar) {  // arrives in every CTA of the unit
+      if constexpr (kPair)
+        mma_commit_pair_elect(bar, static_cast<uint16_t>(0x3u << even));
+      else
+        mma_commit_elect(bar);
+    };
     bool ok = true;
     int s = 0;
     uint32_t turn = 0;
@@ -202,13 +235,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint64_t da = sdesc_sw128(st, 16, 1024);
       const uint64_t db = sdesc_sw128(st + kPBytes, 16, 1024);
 #pragma unroll
-      for (int kk = 0; kk < kK / 16; ++kk)
-        mma_ss_pair_elect(tmem, desc_advance(da, kk * 32), desc_advance(db, kk * 32), idesc,
-                          (ks != k_lo || kk != 0) ? 1u : 0u);
-      mma_commit_pair_elect(bar_empty(s), mask);
+      for (int kk = 0; kk < kK / 16; ++kk) {
+        const uint64_t ak = desc_advance(da, kk * 32), bk = desc_advance(db, kk * 32);
+        const uint32_t more = (ks != k_lo || kk != 0) ? 1u : 0u;
+        if constexpr (kPair)
+          mma_ss_pair_elect(tmem, ak, bk, idesc, more);
+        else
+          mma_ss_elect(tmem, static_cast<uint32_t>(ak), static_cast<uint32_t>(bk),
+                       static_cast<uint32_t>(ak >> 32), idesc, more);
+      }
+      commit(bar_empty(s));
       if (++s == p.stages) s = 0, ++turn;
     }
-    mma_commit_pair_elect(bar_acc, mask);
+    commit(bar_acc);
   }
   // Row r of the partial sums: its token, if it has one.
   auto token_of = [&](int r, int &b, int &s) {
@@ -217,10 +256,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       s = s0 + r;
       return s < p.S;
     } else {
-      // columns: the even CTA's tokens (the first half of every batch element),
-      // then the odd CTA's
-      const int hi = r >= p.Q / 2 ? 1 : 0;
-      const int t = r - hi * (p.Q / 2);
+      // columns: the even CTA's tokens (of a pair the first half of every batch
+      // element), then the odd CTA's
+      const int hi = r >= q_cta ? 1 : 0;
+      const int t = r - hi * q_cta;
       b = p.q_rows == p.Sh ? 0 : t / p.Sh;
       s = hi * p.Sh + t - b * p.Sh;
       return t < p.q_rows && s < p.S;
@@ -238,8 +277,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   __syncwarp();
-  // every MMA of the pair has finished: the accumulator is complete and the
-  // stages free (an aborted pair's MMAs in flight are waited for too)
+  // every MMA of the unit has finished: the accumulator is complete and the
+  // stages free (an aborted unit's MMAs in flight are waited for too)
   bounded(bar_acc, 0);
   tc_fence_after_sync();
   __syncthreads();
@@ -305,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (in && residual != nullptr)
     res = *reinterpret_cast<const uint2 *>(residual + b * p.r_bs + s * p.r_rs + f);
   if (in && epi.gate != nullptr) load_gate(b, s);
-  // where row row_lo of every pair's partial sums lies: this one's own, or
+  // where row row_lo of every unit's partial sums lies: this one's own, or
   // where the others' arrive
   uint32_t sums[kC];
 #pragma unroll
@@ -316,9 +355,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                                                           (row_hi - row_lo)) * p.pitch);
   if constexpr (kC > 1) {
     if (tid < kC && tid != part) {
-      // the rows of pair tid, to the place for this pair's among the others
+      // the rows of unit tid, to the place for this one's among the others
       const int lo = row_of(tid), n = row_of(tid + 1) - lo;
-      const uint32_t to = static_cast<uint32_t>(2 * tid + side);
+      const uint32_t to = rank_of(tid);
       bulk_copy_cluster(
           mapa_shared(sbase + p.recv + static_cast<uint32_t>((part < tid ? part : part - 1) * n) *
                                            p.pitch, to),
@@ -373,22 +412,32 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_wait();  // what this CTA sent has arrived: its shared memory may go
   if (warp == 2) {
     tc_fence_after_sync();
-    tmem_dealloc_pair(tmem, static_cast<uint32_t>(p.tmem_cols));
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem, static_cast<uint32_t>(p.tmem_cols));
+    else
+      tmem_dealloc(tmem, static_cast<uint32_t>(p.tmem_cols));
   }
   if (tid == 0 && *abort_flag) atomicExch(status, FLUX_ERR_DEVICE_TIMEOUT);
 }
 
-// Shared memory of the partial sums of a CTA's rows; of those that arrive.
-uint32_t own_bytes(bool tokens_p, int Q) {
-  return static_cast<uint32_t>(tokens_p ? kP * (Q * 4 + 16) : Q * kP * 4);
+// Rows of a CTA's partial sums and bytes per row.
+int sum_rows(int form, int Q) { return form == kPairX ? kP : Q; }
+uint32_t sum_pitch(int form, int Q) {
+  return static_cast<uint32_t>(form == kPairX ? Q * 4 + 16 : kP * 4);
 }
-uint32_t recv_bytes(bool tokens_p, int Q, int C) {
-  const uint32_t rows = static_cast<uint32_t>(tokens_p ? kP : Q);
-  const uint32_t pitch = static_cast<uint32_t>(tokens_p ? Q * 4 + 16 : kP * 4);
-  return static_cast<uint32_t>(C - 1) * ((rows + C - 1) / C) * pitch;
+// Shared memory of the partial sums of a CTA's rows; of those that arrive.
+uint32_t own_bytes(int form, int Q) {
+  return static_cast<uint32_t>(sum_rows(form, Q)) * sum_pitch(form, Q);
+}
+uint32_t recv_bytes(int form, int Q, int C) {
+  const int rows = sum_rows(form, Q);
+  return static_cast<uint32_t>((C - 1) * ((rows + C - 1) / C)) * sum_pitch(form, Q);
+}
+uint32_t stage_size(int form, int Q) {
+  return kPBytes + static_cast<uint32_t>(form == kSingle ? Q : Q / 2) * kRowBytes;
 }
 
-template <int kAct, bool kTokensP, int kC>
+template <int kAct, int kForm, int kC>
 cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEpilogue &epi,
                    int *status, cudaStream_t stream) {
   static std::once_flag attr_once[64];
@@ -397,7 +446,7 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kernel = linear_split_kernel<kAct, kTokensP, kC>;
+  auto kernel = linear_split_kernel<kAct, kForm, kC>;
   std::call_once(attr_once[dev], [&] {
     attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSmemAll));
@@ -410,33 +459,35 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
   p.o_bs = q.o_bs, p.o_rs = q.o_rs, p.r_bs = q.r_bs, p.r_rs = q.r_rs;
   p.S = static_cast<int>(q.S);
   p.Q = plan.Q;
-  p.Sh = (p.S + 15) / 16 * 8;
-  p.q_rows = kTokensP ? p.Q / 2 : static_cast<int>(q.B) * p.Sh;
-  p.feats = (kTokensP ? p.Q : kP) / (glu ? 2 : 1);
+  p.Sh = kForm == kSingle ? (p.S + 7) / 8 * 8 : (p.S + 15) / 16 * 8;
+  const int q_cta = kForm == kSingle ? p.Q : p.Q / 2;
+  p.q_rows = kForm == kPairX ? q_cta : static_cast<int>(q.B) * p.Sh;
+  p.feats = (kForm == kPairX ? p.Q : kP) / (glu ? 2 : 1);
   p.n_sb = (p.S + 2 * kP - 1) / (2 * kP);
-  const int64_t per_tile = kTokensP ? p.feats : 2 * p.feats;  // features of a pair's tile
+  const int64_t per_tile = kForm == kPairW ? 2 * p.feats : p.feats;  // features of a unit's tile
   const int64_t n_ft = (q.N + per_tile - 1) / per_tile;
-  const int64_t tiles = n_ft * (kTokensP ? q.B * p.n_sb : 1);
-  if (tiles > 0x7FFFFFF || p.q_rows > p.Q / 2) return cudaErrorInvalidValue;
+  const int64_t tiles = n_ft * (kForm == kPairX ? q.B * p.n_sb : 1);
+  if (tiles > 0x7FFFFFF || p.q_rows > q_cta) return cudaErrorInvalidValue;
   p.n_ft = static_cast<int>(n_ft);
   p.tmem_cols = 32;
   while (p.tmem_cols < p.Q) p.tmem_cols *= 2;
   p.nk1 = (q.K + kK - 1) / kK;
   p.nk = p.nk1 + (q.K2 + kK - 1) / kK;
-  p.pitch = static_cast<uint32_t>(kTokensP ? p.Q * 4 + 16 : kP * 4);
+  p.pitch = sum_pitch(kForm, p.Q);
   p.stages = plan.stages;
-  const uint32_t stage = kPBytes + static_cast<uint32_t>(p.Q / 2) * kRowBytes;
   // the CTA's own partial sums over the drained ring, the others' behind them
-  const uint32_t ring = static_cast<uint32_t>(p.stages) * stage;
-  const uint32_t own = own_bytes(kTokensP, p.Q);
+  const uint32_t ring = static_cast<uint32_t>(p.stages) * stage_size(kForm, p.Q);
+  const uint32_t own = own_bytes(kForm, p.Q);
   p.early = plan.early ? 1 : 0;
   p.recv = plan.early ? std::max(ring, own) : own;
-  p.tail = std::max(ring, p.recv + recv_bytes(kTokensP, p.Q, kC));
-  const uint32_t smem = p.tail + kTailBytes;
-  if (smem > kSmemAll) return cudaErrorInvalidValue;
-  const uint32_t w_box = static_cast<uint32_t>(kTokensP ? p.Q / 2 : p.feats);
-  const uint32_t x_box = static_cast<uint32_t>(kTokensP ? kP : p.Sh);
-  const uint32_t x_box_b = kTokensP ? 1 : static_cast<uint32_t>(q.B);
+  p.tail = std::max(ring, p.recv + recv_bytes(kForm, p.Q, kC));
+  const uint32_t need = p.tail + kTailBytes;
+  // a pair's CTA takes more than half an SM's shared memory, whatever it needs
+  const uint32_t smem = kForm == kSingle ? need : std::max(need, kSmemHalf + 4096);
+  if (smem > (kForm == kSingle ? kSmemHalf : kSmemAll)) return cudaErrorInvalidValue;
+  const uint32_t w_box = static_cast<uint32_t>(kForm == kPairX ? p.Q / 2 : p.feats);
+  const uint32_t x_box = static_cast<uint32_t>(kForm == kPairX ? kP : p.Sh);
+  const uint32_t x_box_b = kForm == kPairX ? 1 : static_cast<uint32_t>(q.B);
   SplitMaps maps;
   const uint16_t *w2 = static_cast<const uint16_t *>(q.w) + q.K;
   if (!make_row_map(&maps.x, q.x, q.K, q.S, q.B, q.x_rs, q.x_bs, kK, x_box, x_box_b) ||
@@ -451,12 +502,12 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * kC;
+  attr[0].val.clusterDim.x = kForm == kSingle ? kC : 2 * kC;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * 2 * kC), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles) * attr[0].val.clusterDim.x, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -467,32 +518,41 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
                             static_cast<uint16_t *>(q.out), status);
 }
 
-template <int kAct, bool kTokensP>
+template <int kAct, int kForm>
 cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEpilogue &epi,
                    int *status, cudaStream_t stream) {
   switch (plan.C) {
-    case 1: return launch<kAct, kTokensP, 1>(q, plan, epi, status, stream);
-    case 2: return launch<kAct, kTokensP, 2>(q, plan, epi, status, stream);
-    case 3: return launch<kAct, kTokensP, 3>(q, plan, epi, status, stream);
-    default: return launch<kAct, kTokensP, 4>(q, plan, epi, status, stream);
+    case 1: return launch<kAct, kForm, 1>(q, plan, epi, status, stream);
+    case 2: return launch<kAct, kForm, 2>(q, plan, epi, status, stream);
+    case 3: return launch<kAct, kForm, 3>(q, plan, epi, status, stream);
+    case 4: return launch<kAct, kForm, 4>(q, plan, epi, status, stream);
+    default: break;
   }
+  if constexpr (kForm == kSingle) {
+    if (plan.C == 6) return launch<kAct, kForm, 6>(q, plan, epi, status, stream);
+    if (plan.C == 8) return launch<kAct, kForm, 8>(q, plan, epi, status, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 template <int kAct>
 cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEpilogue &epi,
                    int *status, cudaStream_t stream) {
-  return plan.tokens_p ? launch<kAct, true>(q, plan, epi, status, stream)
-                       : launch<kAct, false>(q, plan, epi, status, stream);
+  switch (plan.form) {
+    case kSingle: return launch<kAct, kSingle>(q, plan, epi, status, stream);
+    case kPairW: return launch<kAct, kPairW>(q, plan, epi, status, stream);
+    default: return launch<kAct, kPairX>(q, plan, epi, status, stream);
+  }
 }
 
 }  // namespace
 
-// The tile, the split of the channels and the ring. A launch has so many CTAs
-// resident: with all of an SM's shared memory each (clusters of 4, 6 and 8 do
-// not fill every SM), or with half of it. Half leaves room for the next
-// kernel's prologue, and for a second CTA, which helps where one wave of whole
-// SMs is not enough; but then two CTAs share what the SM takes in, and a ring
-// of half the bytes is refilled only every 1.1 us.
+// The form, the split of the channels and the ring. A launch has so many CTAs
+// resident, by the CTAs of a cluster: those of pairs have an SM each (clusters
+// of 4, 6 and 8 do not fill every SM), single ones half an SM. Half an SM
+// leaves room for the next kernel's prologue and for a second CTA; but then
+// the two share what the SM takes in, and a ring of half the bytes is refilled
+// only every 1.1 us.
 SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
   const bool glu = act == FLUX_ACT_SWIGLU;
   const int64_t nk = (q.K + kK - 1) / kK + (q.K2 + kK - 1) / kK;
@@ -500,48 +560,47 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
   const double bytes = 2.0 * (static_cast<double>(q.B * q.S + wr) * (q.K + q.K2) +
                               static_cast<double>(q.B * q.S) * q.N *
                                   (q.residual != nullptr ? 2 : 1));
-  static constexpr int kWhole[kMaxC] = {152, 144, 138, 120}, kHalf[kMaxC] = {304, 296, 276, 288};
-  SplitPlan best{false, false, 32, 1, 2, 1e30};
-  auto consider = [&](bool tokens_p, int Q) {
-    const int64_t feats = (tokens_p ? Q : 2 * kP) / (glu ? 2 : 1);  // of a tile
-    const int64_t tiles =
-        (q.N + feats - 1) / feats * (tokens_p ? q.B * ((q.S + 2 * kP - 1) / (2 * kP)) : 1);
-    const uint32_t stage = kPBytes + static_cast<uint32_t>(Q / 2) * kRowBytes;
-    const int rows = tokens_p ? kP : Q;
-    const int cta_feats = (tokens_p ? Q : kP) / (glu ? 2 : 1);
-    const double pitch = tokens_p ? Q * 4 + 16 : kP * 4;
-    for (int C = 1; C <= kMaxC && C <= nk; ++C) {
-      const uint32_t recv = recv_bytes(tokens_p, Q, C);
-      const int64_t ctas = tiles * 2 * C;
-      const int64_t whole = kWhole[C - 1] * static_cast<int64_t>(sms) / 152;
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t room = (half ? kSmemHalf : kSmemAll) - kTailBytes;
-        if (own_bytes(tokens_p, Q) + recv > room || 3 * stage > room) continue;
-        int stages = static_cast<int>(std::min<uint32_t>(kMaxStages, room / stage));
-        // a place of their own for the sums saves a cluster barrier, unless the
-        // ring gets short for it
-        const bool early = recv + kEarlyRing <= room;
-        if (early)
-          stages = static_cast<int>(std::min<uint32_t>(kMaxStages, (room - recv) / stage));
-        const int64_t slots = half ? kHalf[C - 1] * static_cast<int64_t>(sms) / 152 : whole;
-        const double waves = static_cast<double>((ctas + slots - 1) / slots);
-        const double shared =
-            !half ? 1.0 : std::min(ctas, slots) > sms ? 2.0 : ctas > whole ? 1.4 : 1.0;
-        const double per_stage =
-            std::max(stage_ns(stage, Q) * shared, 1090.0 / static_cast<double>(stages));
-        const double ns =
-            std::max(waves * static_cast<double>((nk + C - 1) / C) * per_stage, bytes / 9000.0) +
-            waves * 2130.0 + 2100.0 - (half && ctas <= whole ? 260.0 : 0.0) +
-            (C > 1 ? 520.0 + (C - 1) * (rows / static_cast<double>(C)) * pitch / 65.0 : 0.0) +
-            0.17 * rows / C * cta_feats;
-        if (ns < best.ns) best = SplitPlan{tokens_p, early, Q, C, stages, ns};
-      }
+  static constexpr int kResident[2][9] = {{0, 152, 152, 0, 144, 0, 138, 0, 120},    // an SM each
+                                          {0, 304, 304, 291, 296, 0, 276, 0, 288}};  // half an SM
+  SplitPlan best{kPairX, false, 32, 1, 2, 1e30};
+  auto consider = [&](int form, int Q) {
+    const bool single = form == kSingle;
+    const int64_t feats = (form == kPairX ? Q : single ? kP : 2 * kP) / (glu ? 2 : 1);
+    const int64_t tiles = (q.N + feats - 1) / feats *
+                          (form == kPairX ? q.B * ((q.S + 2 * kP - 1) / (2 * kP)) : 1);
+    const int rows = sum_rows(form, Q);
+    const int cta_feats = (form == kPairX ? Q : kP) / (glu ? 2 : 1);
+    const uint32_t stage = stage_size(form, Q);
+    const uint32_t room = (single ? kSmemHalf : kSmemAll) - kTailBytes;
+    for (int C = 1; C <= max_units(form) && C <= nk; ++C) {
+      const int size = single ? C : 2 * C;  // CTAs of a cluster
+      const int64_t slots = kResident[single ? 1 : 0][size] * static_cast<int64_t>(sms) / 152;
+      const uint32_t recv = recv_bytes(form, Q, C);
+      if (slots < size || own_bytes(form, Q) + recv > room || 3 * stage > room) continue;
+      int stages = static_cast<int>(std::min<uint32_t>(kMaxStages, room / stage));
+      // a place of their own for the sums saves a cluster barrier, unless the
+      // ring gets short for it
+      const bool early = recv + kEarlyRing <= room;
+      if (early) stages = static_cast<int>(std::min<uint32_t>(kMaxStages, (room - recv) / stage));
+      const int64_t ctas = tiles * size;
+      const double waves = static_cast<double>((ctas + slots - 1) / slots);
+      const double shared = !single || ctas <= sms ? 1.0 : std::min(2.0, ctas / (0.75 * sms));
+      const double per_stage =
+          std::max(stage_ns(stage, single ? Q / 2 : Q) * shared, 1090.0 / stages);
+      const double ns =
+          std::max(waves * static_cast<double>((nk + C - 1) / C) * per_stage, bytes / 9000.0) +
+          waves * 2130.0 + 2100.0 - (single ? 260.0 : 0.0) +
+          (C > 1 ? 520.0 + (C - 1) * (rows / static_cast<double>(C)) * sum_pitch(form, Q) / 65.0
+                 : 0.0) +
+          0.17 * rows / C * cta_feats;
+      if (ns < best.ns) best = SplitPlan{form, early, Q, C, stages, ns};
     }
   };
-  const int64_t rows_q = q.B * ((q.S + 15) / 16 * 16);
-  if (rows_q <= 256) consider(false, static_cast<int>((rows_q + 31) / 32 * 32));
+  const int64_t rows8 = q.B * ((q.S + 7) / 8 * 8), rows16 = q.B * ((q.S + 15) / 16 * 16);
+  if (rows8 <= 64) consider(kSingle, static_cast<int>((rows8 + 15) / 16 * 16));
+  if (rows16 <= 256) consider(kPairW, static_cast<int>((rows16 + 31) / 32 * 32));
   if (q.B * q.S >= 64)  // fewer tokens would fill less than a quarter of P
-    for (int Q = 32; Q <= 256; Q += 32) consider(true, Q);
+    for (int Q = 32; Q <= 256; Q += 32) consider(kPairX, Q);
   return best;
 }
 

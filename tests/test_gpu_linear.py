@@ -344,3 +344,29 @@ def test_drawn_problems(B, S, K, N, kw, strided):
                                        ops[name]], 1)[:, 1:]
     out = torch.full((B, S + 2, N), 7.0, dtype=torch.bfloat16, device="cuda")[:, 1:-1]
     R.check(_run(ops, out=out), R.linear(**ops), f"{B}x{S}x{K}->{N}")
+
+
+def test_small_calls_in_a_row_and_side_by_side():
+    """Calls of every form back to back on two streams: prologues overlap the
+    kernels before them and tiles of different calls share SMs; every call ends
+    and is right."""
+    probs = [_make(1, 16, 512, 8192, act="silu", bias=True, seed=1),
+             _make(2, 1, 256, 4096, seed=2),
+             _make(1, 200, 512, 1024, gate=True, residual=True, seed=3),
+             _make(1, 384, 1024, 1024, act="swiglu", seed=4),
+             _make(1, 512, 256, 2048, residual=True, seed=5)]
+    want = [R.linear(**ops) for ops in probs]
+    outs = [[torch.empty_like(w[0], dtype=torch.bfloat16, device="cuda") for w in want]
+            for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(60):
+        for st, out in zip(streams, outs):
+            with torch.cuda.stream(st):
+                for k in range(len(probs)):
+                    j = (i * (k + 1) + k) % len(probs)
+                    binding.linear(**probs[j], out=out[j])
+    torch.cuda.synchronize()
+    for out in outs:
+        for o, w in zip(out, want):
+            R.check(o, w, "side by side")

@@ -20,13 +20,14 @@ PAIR = ("linear_pair_sm103a.cu",
         "if (lane == 0 && lt != 0) "
         "mbar_arrive_cluster(acc_empty0 + 8u * static_cast<uint32_t>(lt & 1));")
 # the MMA warp's release of a stage (the producers wait to fill it again)
-SPLIT = ("linear_split_sm103a.cu", "mma_commit_pair_elect(bar_empty(s), mask);",
-         "if (turn != 0) mma_commit_pair_elect(bar_empty(s), mask);")
+SPLIT = ("linear_split_sm103a.cu", "commit(bar_empty(s));",
+         "if (turn != 0) commit(bar_empty(s));")
 
 
 @pytest.mark.parametrize("patch,S,K,N,vecs", [(PAIR, 2600, 64, 4096, False),
                                               (PAIR, 2600, 64, 4096, True),
-                                              (SPLIT, 9, 4096, 256, True)])
+                                              (SPLIT, 9, 8192, 256, True),     # single CTAs
+                                              (SPLIT, 100, 8192, 256, True)])  # CTA pairs
 def test_bounded_wait_reports_timeout_and_context_survives(tmp_path, patch, S, K, N, vecs):
     build.build()
     binding.load()
