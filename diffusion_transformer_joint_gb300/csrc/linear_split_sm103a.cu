@@ -29,7 +29,8 @@
 // A CTA pair has its two SMs to itself. Two pairs on the same SMs would
 // allocate TMEM for both SMs at the same time, and an SM lets one CTA allocate
 // until that one is done: each pair could hold one SM and wait for the other
-// for ever. Two CTAs share an SM only where each allocates for itself.
+// for ever (pairs with half an SM's memory each did hang, once in some 10^5
+// calls). Two CTAs share an SM only where each allocates for itself.
 //
 // 16 warps: warp 0 TMA producer, warp 1 MMA issuer (of the pair's even CTA; one
 // K16 MMA per 16 channels), warp 2 TMEM allocation; then all of them move the
@@ -58,6 +59,9 @@ constexpr int max_units(int form) { return form == kSingle ? kMaxUnits : kMaxUni
 constexpr int kThreads = 512;
 constexpr uint32_t kSmemAll = 232448;   // a pair's CTAs: one per SM
 constexpr uint32_t kSmemHalf = 114688;  // single CTAs: two per SM
+// A pair's CTA takes no less: beside it an SM has no room for another CTA that
+// allocates TMEM (a single one's ring takes 96 KB or more).
+constexpr uint32_t kSmemPair = 147456;
 constexpr uint32_t kTailBytes = 256;    // barriers and flags
 // A ring that sums may have a place of their own beside: with less on its way
 // than about 1.5 us of what an SM takes in, the stages wait for the memory.
@@ -482,8 +486,7 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
   p.recv = plan.early ? std::max(ring, own) : own;
   p.tail = std::max(ring, p.recv + recv_bytes(kForm, p.Q, kC));
   const uint32_t need = p.tail + kTailBytes;
-  // a pair's CTA takes more than half an SM's shared memory, whatever it needs
-  const uint32_t smem = kForm == kSingle ? need : std::max(need, kSmemHalf + 4096);
+  const uint32_t smem = kForm == kSingle ? need : std::max(need, kSmemPair);
   if (smem > (kForm == kSingle ? kSmemHalf : kSmemAll)) return cudaErrorInvalidValue;
   const uint32_t w_box = static_cast<uint32_t>(kForm == kPairX ? p.Q / 2 : p.feats);
   const uint32_t x_box = static_cast<uint32_t>(kForm == kPairX ? kP : p.Sh);
