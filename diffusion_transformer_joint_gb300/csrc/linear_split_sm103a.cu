@@ -74,7 +74,8 @@ struct SplitShape {
   int q_rows;      // rows of Q that each CTA copies
   int Sh;          // tokens as Q: a batch element's in one CTA, rounded up to 8
   int n_sb;        // tokens as P: 256-row blocks per batch element
-  int n_ft;        // feature tiles
+  int n_tb;        // tokens as P: 256-row blocks; those of one feature tile are
+                   // neighbours and read its W from L2
   int feats;       // output features of a CTA's tile
   int nk1, nk;     // stages of x, in all
   int stages, tmem_cols;
@@ -129,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   // the tile: its first feature, and with tokens as P its batch element and
   // this CTA's first token
   const int tile = static_cast<int>(cluster_id_x());
-  const int tb = tile / p.n_ft;
-  const int ft = tile - tb * p.n_ft;
+  const int ft = kTokensP ? tile / p.n_tb : tile;
+  const int tb = tile - ft * p.n_tb;  // (tokens as P)
   const int64_t f0 = static_cast<int64_t>(kForm == kPairW ? 2 * ft + side : ft) * p.feats;
   const int b0 = kTokensP ? tb / p.n_sb : 0;
   const int s0 = kTokensP ? ((tb - b0 * p.n_sb) * 2 + side) * kP : 0;
@@ -472,7 +473,7 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
   const int64_t n_ft = (q.N + per_tile - 1) / per_tile;
   const int64_t tiles = n_ft * (kForm == kPairX ? q.B * p.n_sb : 1);
   if (tiles > 0x7FFFFFF || p.q_rows > q_cta) return cudaErrorInvalidValue;
-  p.n_ft = static_cast<int>(n_ft);
+  p.n_tb = static_cast<int>(kForm == kPairX ? q.B * p.n_sb : 1);
   p.tmem_cols = 32;
   while (p.tmem_cols < p.Q) p.tmem_cols *= 2;
   p.nk1 = (q.K + kK - 1) / kK;
