@@ -556,7 +556,7 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
 // of 4, 6 and 8 do not fill every SM), single ones half an SM. Half an SM
 // leaves room for the next kernel's prologue and for a second CTA; but then
 // the two share what the SM takes in, and a ring of half the bytes is refilled
-// only every 1.3 us.
+// only every 1.4 us.
 SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
   const bool glu = act == FLUX_ACT_SWIGLU;
   const int64_t nk = (q.K + kK - 1) / kK + (q.K2 + kK - 1) / kK;
@@ -566,13 +566,14 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
                                   (q.residual != nullptr ? 2 : 1));
   static constexpr int kResident[2][9] = {{0, 152, 152, 0, 144, 0, 138, 0, 120},    // an SM each
                                           {0, 304, 304, 291, 296, 0, 276, 0, 288}};  // half an SM
-  // ns: to refill a ring, a wave, a call, to join sums, to finish one;
-  // bytes per ns: of the memory, of sums between CTAs
+  // ns: to refill a ring (what a pair's brings hides it), a wave, a call, a row
+  // of Q, to join sums, to finish one; bytes per ns: of the memory, of sums
+  // between CTAs
   struct Costs {
-    double refill, wave, call, join, finish, hbm, send;
+    double refill, wave, call, row, join, finish, hbm, send;
   };
-  static constexpr Costs kPairCosts = {1090.0, 2130.0, 2100.0, 520.0, 0.17, 9000.0, 65.0};
-  static constexpr Costs kSingleCosts = {1340.0, 3760.0, -440.0, 180.0, 0.05, 8000.0, 26.0};
+  static constexpr Costs kPairCosts = {0.0, 4540.0, 250.0, 0.0, 480.0, 0.077, 18000.0, 160.0};
+  static constexpr Costs kSingleCosts = {1410.0, 4830.0, -1880.0, 17.5, 160.0, 0.043, 7600.0, 67.0};
   SplitPlan best{kPairX, false, 32, 1, 2, 1e30};
   auto consider = [&](int form, int Q) {
     const bool single = form == kSingle;
@@ -595,13 +596,13 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
       if (early) stages = static_cast<int>(std::min<uint32_t>(kMaxStages, (room - recv) / stage));
       const int64_t ctas = tiles * size;
       const double waves = static_cast<double>((ctas + slots - 1) / slots);
-      const double shared = !single || ctas <= sms ? 1.0 : std::min(2.0, ctas / (0.81 * sms));
+      const double shared = !single || ctas <= sms ? 1.0 : std::min(2.0, ctas / (0.66 * sms));
       const Costs &t = single ? kSingleCosts : kPairCosts;
       const double per_stage =
           std::max(stage_ns(stage, single ? Q / 2 : Q) * shared, t.refill / stages);
       const double ns =
           std::max(waves * static_cast<double>((nk + C - 1) / C) * per_stage, bytes / t.hbm) +
-          waves * t.wave + t.call +
+          waves * t.wave + t.call + t.row * Q +
           (C > 1 ? t.join + (C - 1) * (rows / static_cast<double>(C)) * sum_pitch(form, Q) / t.send
                  : 0.0) +
           t.finish * rows / C * cta_feats;
