@@ -165,8 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // both CTAs' barriers are initialised before either signals the other's
   tc_fence_before_sync();
-  __syncwarp();
-  cluster_sync_all();
+  cluster_sync_relaxed();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   grid_dep_launch_dependents();
@@ -418,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
-  // neither CTA leaves while the other may still signal its barriers or
-  // read its shared memory
+  // neither CTA leaves while the other may still signal its barriers or read
+  // its shared memory (signals under way count: a barrier with release)
   tc_fence_before_sync();
   __syncwarp();
   cluster_sync_all();
