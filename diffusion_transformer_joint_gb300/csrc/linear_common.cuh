@@ -58,12 +58,19 @@ __device__ __forceinline__ void load_vec8(const void *base, int64_t off, int f32
   }
 }
 
-// Four entries, 8-byte (bf16) or 16-byte (fp32) aligned.
-__device__ __forceinline__ float4 load_vec4(const void *base, int64_t off, int f32) {
-  if (f32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
+// Four entries, 8-byte (bf16) or 16-byte (fp32) aligned, as stored; and their
+// values, for when they have arrived.
+__device__ __forceinline__ uint4 load_raw4(const void *base, int64_t off, int f32) {
+  if (f32) return *reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + off);
   const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + off);
-  return make_float4(bf16lo_to_f32(w.x), bf16hi_to_f32(w.x), bf16lo_to_f32(w.y),
-                     bf16hi_to_f32(w.y));
+  return make_uint4(w.x, w.y, 0u, 0u);
+}
+__device__ __forceinline__ float4 raw4_values(uint4 v, int f32) {
+  if (f32)
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                       __uint_as_float(v.w));
+  return make_float4(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y),
+                     bf16hi_to_f32(v.y));
 }
 
 __device__ __forceinline__ float load_vec1(const void *base, int64_t off, int f32) {

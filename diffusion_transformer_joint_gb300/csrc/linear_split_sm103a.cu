@@ -100,7 +100,7 @@ __device__ __forceinline__ void add4(float4 &v, float4 a) {
 }
 
 template <int kAct, int kForm, int kC>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kForm == kSingle ? 2 : 1)
     linear_split_kernel(const __grid_constant__ SplitMaps maps, const SplitShape p,
                         const LinearEpilogue epi, const uint16_t *residual, uint16_t *out,
                         int *status) {
@@ -181,6 +181,48 @@ __global__ void __launch_bounds__(kThreads, 2)
   // everything up to here overlaps the end of the kernel before this one
   grid_dep_wait();
 
+  // Row r of the partial sums: its token, if it has one.
+  auto token_of = [&](int r, int &b, int &s) {
+    if constexpr (kTokensP) {
+      b = b0;
+      s = s0 + r;
+      return s < p.S;
+    } else {
+      // columns: the even CTA's tokens (of a pair the first half of every batch
+      // element), then the odd CTA's
+      const int hi = r >= q_cta ? 1 : 0;
+      const int t = r - hi * q_cta;
+      b = p.q_rows == p.Sh ? 0 : t / p.Sh;
+      s = hi * p.Sh + t - b * p.Sh;
+      return t < p.q_rows && s < p.S;
+    }
+  };
+  // A thread finishes four features of tokens `per` apart, from row r of the
+  // partial sums on. Their bias and the first one's gate come while the tile
+  // is computed (loaded at its end they cost 0.3 to 0.6 us of a call).
+  const int n_quad = p.feats / 4;
+  const int per = kThreads / n_quad;
+  const int o = tid % n_quad;
+  const int64_t f = f0 + o * 4;
+  const bool mine = tid < per * n_quad && f < p.N;
+  int r = row_lo + tid / n_quad;
+  int b, s;
+  uint4 bias_raw = make_uint4(0u, 0u, 0u, 0u), bias_u_raw = bias_raw, gate_raw = bias_raw;
+  uint32_t gate_row = 0xFFFFFFFFu;  // of gate_raw
+  auto load_gate = [&] {            // of token (b, s)
+    // joined batch elements (at most 2^30 tokens) are found by division
+    const uint32_t row = epi.gate_rows == p.S
+                             ? static_cast<uint32_t>(b)
+                             : static_cast<uint32_t>(s) / static_cast<uint32_t>(epi.gate_rows);
+    if (row != gate_row) gate_raw = load_raw4(epi.gate, row * epi.gate_bs + f, epi.vec_f32);
+    gate_row = row;
+  };
+  if (mine && epi.bias != nullptr) {
+    bias_raw = load_raw4(epi.bias, f, epi.vec_f32);
+    if constexpr (kGlu) bias_u_raw = load_raw4(epi.bias, p.N + f, epi.vec_f32);
+  }
+  if (mine && epi.gate != nullptr && r < row_hi && token_of(r, b, s)) load_gate();
+
   if (warp == 0 && lane == 0) {
     const uint32_t bytes = kPBytes + static_cast<uint32_t>(p.q_rows) * kRowBytes;
     const int x0 = kTokensP ? s0 : side * p.Sh;
@@ -253,22 +295,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     commit(bar_acc);
   }
-  // Row r of the partial sums: its token, if it has one.
-  auto token_of = [&](int r, int &b, int &s) {
-    if constexpr (kTokensP) {
-      b = b0;
-      s = s0 + r;
-      return s < p.S;
-    } else {
-      // columns: the even CTA's tokens (of a pair the first half of every batch
-      // element), then the odd CTA's
-      const int hi = r >= q_cta ? 1 : 0;
-      const int t = r - hi * q_cta;
-      b = p.q_rows == p.Sh ? 0 : t / p.Sh;
-      s = hi * p.Sh + t - b * p.Sh;
-      return t < p.q_rows && s < p.S;
-    }
-  };
   if (warp >= 4 && residual != nullptr) {
     // the residual's lines, wanted at the end, come to L2 meanwhile
     const int lines = (p.feats + 63) / 64;
@@ -317,40 +343,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     cluster_sync_relaxed();
   else
     __syncthreads();
-  // A thread finishes four features of tokens `per` apart. The loop is short
-  // and its latencies are left to the 16 warps: this code runs once, and
-  // unrolled it cost more in instruction misses than it saved.
-  const int n_quad = p.feats / 4;
-  const int per = kThreads / n_quad;
-  const int o = tid % n_quad;
-  const int64_t f = f0 + o * 4;
-  const bool mine = tid < per * n_quad && f < p.N;
-  float4 bias = make_float4(0.f, 0.f, 0.f, 0.f), bias_u = bias;
-  if (mine && epi.bias != nullptr) {
-    bias = load_vec4(epi.bias, f, epi.vec_f32);
-    if constexpr (kGlu) bias_u = load_vec4(epi.bias, p.N + f, epi.vec_f32);
-  }
-  // the first tokens' residual and the gate come while the sums arrive
-  float4 gate = bias;
-  uint32_t gate_row = 0xFFFFFFFFu;  // of `gate`
-  auto load_gate = [&](int b, int s) {
-    // joined batch elements (at most 2^30 tokens) are found by division
-    const uint32_t row = epi.gate_rows == p.S
-                             ? static_cast<uint32_t>(b)
-                             : static_cast<uint32_t>(s) / static_cast<uint32_t>(epi.gate_rows);
-    if (row != gate_row) gate = load_vec4(epi.gate, row * epi.gate_bs + f, epi.vec_f32);
-    gate_row = row;
-  };
-  int r = row_lo + tid / n_quad;
-  int b, s;
-  auto fetch = [&](int row) {  // row's residual: three on their way at a time
+  // the residual of the first tokens comes while the sums arrive
+  auto fetch = [&](int row) {  // row's residual: three are on their way at a time
     uint2 v = make_uint2(0u, 0u);
     if (mine && residual != nullptr && row < row_hi && token_of(row, b, s))
       v = *reinterpret_cast<const uint2 *>(residual + b * p.r_bs + s * p.r_rs + f);
     return v;
   };
   uint2 res = fetch(r), res1 = fetch(r + per), res2 = fetch(r + 2 * per);
-  if (epi.gate != nullptr && mine && r < row_hi && token_of(r, b, s)) load_gate(b, s);
   // where row row_lo of every unit's partial sums lies: this one's own, or
   // where the others' arrive
   uint32_t sums[kC];
@@ -382,7 +382,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_arrive_relaxed();  // what was sent to this CTA has arrived
 
   if (mine) {
+    const float4 bias = raw4_values(bias_raw, epi.vec_f32);
+    const float4 bias_u = raw4_values(bias_u_raw, epi.vec_f32);
     const uint32_t half = static_cast<uint32_t>(p.feats) * 4;  // SwiGLU: to the linear sums
+    // a short loop, its latencies left to the 16 warps: this code runs once, and
+    // unrolled it cost more in instruction misses than it saved
 #pragma unroll 1
     for (; r < row_hi; r += per) {
       const uint2 res_next = fetch(r + 3 * per);
@@ -401,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           y = make_float4(activate<kAct>(y.x), activate<kAct>(y.y), activate<kAct>(y.z),
                           activate<kAct>(y.w));
         if (epi.gate != nullptr) {
-          load_gate(b, s);
+          load_gate();
+          const float4 gate = raw4_values(gate_raw, epi.vec_f32);
           y.x *= gate.x, y.y *= gate.y, y.z *= gate.z, y.w *= gate.w;
         }
         if (residual != nullptr)
