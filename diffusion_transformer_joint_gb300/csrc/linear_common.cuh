@@ -92,9 +92,9 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 
 // What the plans' estimates (ns) share: an SM takes in about 112 bytes per ns;
 // a stage's 64 channels are four MMAs of N / 2 cycles, about N ns. Fitted, like
-// the constants beside them, to the times of every form at 112 problems of 1 to
+// the constants beside them, to the times of every form at 103 problems of 1 to
 // 4608 rows: the form that the estimates pick takes 1.01 times the best one's
-// time (geometric mean; at most 1.23).
+// time (geometric mean; at most 1.17).
 constexpr double kBytesPerNs = 112.0;
 inline double stage_ns(double bytes, int n) {
   return bytes / kBytesPerNs > n ? bytes / kBytesPerNs : n;

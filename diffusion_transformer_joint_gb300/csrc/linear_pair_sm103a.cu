@@ -546,8 +546,8 @@ PairPlan plan_pair(const LinearProblem &q, int act, int sms) {
     const int64_t feats = glu ? tn / 2 : tn;
     const int64_t tiles = n_rb * ((q.N + feats - 1) / feats);
     const double waves = static_cast<double>((tiles + pairs - 1) / pairs);
-    const double ns = waves * (nk * stage_ns(kABytes + tn / 2 * kBRowBytes, tn) + 80.0) +
-                      3735.0 + 10.7 * tn;
+    const double ns = waves * (nk * stage_ns(kABytes + tn / 2 * kBRowBytes, tn) + 66.0) +
+                      3640.0 + 9.7 * tn;
     if (ns < best.ns) best = PairPlan{tn, ns};
   }
   return best;

@@ -561,7 +561,7 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
 // of 4, 6 and 8 do not fill every SM), single ones half an SM. Half an SM
 // leaves room for the next kernel's prologue and for a second CTA; but then
 // the two share what the SM takes in, and a ring of half the bytes is refilled
-// only every 1.4 us.
+// only every 1.3 us.
 SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
   const bool glu = act == FLUX_ACT_SWIGLU;
   const int64_t nk = (q.K + kK - 1) / kK + (q.K2 + kK - 1) / kK;
@@ -577,8 +577,8 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
   struct Costs {
     double refill, wave, call, row, join, finish, hbm, send;
   };
-  static constexpr Costs kPairCosts = {0.0, 4540.0, 250.0, 0.0, 480.0, 0.077, 18000.0, 160.0};
-  static constexpr Costs kSingleCosts = {1410.0, 4830.0, -1880.0, 17.5, 160.0, 0.043, 7600.0, 67.0};
+  static constexpr Costs kPairCosts = {0.0, 4100.0, 240.0, 0.0, 330.0, 0.056, 23000.0, 123.0};
+  static constexpr Costs kSingleCosts = {1275.0, 4720.0, -2210.0, 16.0, 158.0, 0.046, 7860.0, 92.0};
   SplitPlan best{kPairX, false, 32, 1, 2, 1e30};
   auto consider = [&](int form, int Q) {
     const bool single = form == kSingle;
@@ -601,7 +601,7 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
       if (early) stages = static_cast<int>(std::min<uint32_t>(kMaxStages, (room - recv) / stage));
       const int64_t ctas = tiles * size;
       const double waves = static_cast<double>((ctas + slots - 1) / slots);
-      const double shared = !single || ctas <= sms ? 1.0 : std::min(2.0, ctas / (0.66 * sms));
+      const double shared = !single || ctas <= sms ? 1.0 : std::min(2.0, ctas / (0.59 * sms));
       const Costs &t = single ? kSingleCosts : kPairCosts;
       const double per_stage =
           std::max(stage_ns(stage, single ? Q / 2 : Q) * shared, t.refill / stages);
