@@ -386,7 +386,13 @@ __global__ void __launch_bounds__(kThreads, kForm == kSingle ? 2 : 1)
             static_cast<uint32_t>(q_n) * p.pitch, mapa_shared(bar_recv, to));
     }
     __syncwarp();
-    if (!mbar_wait_cluster(bar_recv, 0, abort_flag)) *abort_flag = 1;
+    // An abort does not end this wait: every unit sends its rows, an aborted one
+    // too, and they must have arrived before this CTA lets the cluster go. The
+    // last unit may have waited for a stage and then for its copies, a budget
+    // each, since this one was done.
+    if (!mbar_try_wait_cluster(bar_recv, 0) &&
+        !mbar_settled(bar_recv, 0, clock64() + 4 * kWaitBudgetCycles))
+      *abort_flag = 1;
   }
   __syncwarp();
   cluster_arrive_relaxed();  // what was sent to this CTA has arrived

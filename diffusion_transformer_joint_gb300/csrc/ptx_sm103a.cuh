@@ -407,6 +407,14 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     }
   }
 }
+// Bounded wait for what has to have ended before the CTA goes on even after an
+// abort (copies and MMAs in flight): the abort flag does not cut it short, the
+// clock does at `until`. Returns true on completion.
+__device__ __forceinline__ bool mbar_settled(uint32_t bar, uint32_t parity, long long until) {
+  while (!mbar_try_wait_cluster(bar, parity))
+    if (clock64() > until) return false;
+  return true;
+}
 // 2-D tiled tensor copy into this CTA's shared memory whose completion is
 // counted on an mbarrier of either CTA of the pair (cluster-window address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *tmap,

@@ -1,0 +1,106 @@
+"""What flux_linear's kernels leave behind when a bounded wait runs out. No GPU
+fault is made: a copy of the library withholds one hand-off, so that the wait
+ends by its clock, and the copy's kernel reports what it finds at its end."""
+import ctypes
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+from diffusion_transformer_joint_gb300 import binding, build
+from tests import block_reference as R
+
+pytestmark = pytest.mark.gpu
+
+TIMEOUT = -7
+NOT_LANDED = -77  # reported by the copy's kernel, in place of the timeout
+# the kernels' own report, made not to cover the copy's
+REPORT = ("if (tid == 0 && *abort_flag) atomicExch(status,",
+          "if (tid == 0 && *abort_flag) atomicMin(status,")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+    binding.load()
+
+
+_built = {}
+
+
+def _patched(tmp_path, name, patches):
+    """flux_linear of a copy of the library with `patches` made in one source."""
+    key = (name, tuple(patches))
+    if key not in _built:
+        _built[key] = _build_patched(tmp_path, name, patches)
+    return _built[key]
+
+
+def _build_patched(tmp_path, name, patches):
+    src = tmp_path / "csrc"
+    shutil.copytree(build.CSRC, src)
+    text = (src / name).read_text()
+    for anchor, new in patches:
+        assert text.count(anchor) == 1, f"not found exactly once: {anchor}"
+        text = text.replace(anchor, new)
+    (src / name).write_text(text)
+    out = tmp_path / "libflux_patched.so"
+    flags = [x for x in build.NVCC_FLAGS if x not in ("-Xptxas", "-v")]
+    subprocess.run([build.nvcc(), *flags, "-I", build.INCLUDE, "-I", str(src),
+                    *sorted(str(p) for p in src.glob("*.cu")), "-o", str(out)],
+                   check=True, capture_output=True)
+    lib = ctypes.CDLL(str(out))
+    lib.flux_linear.argtypes = binding.load().flux_linear.argtypes
+    lib.flux_linear.restype = ctypes.c_int
+    return lib.flux_linear
+
+
+def _problem(S, K, N):
+    g = torch.Generator().manual_seed(71)
+    x = torch.randn(1, S, K, generator=g).bfloat16().cuda()
+    w = (torch.randn(N, K, generator=g) * K ** -0.5).bfloat16().cuda()
+    return x, w, torch.randn(1, S, N, generator=g).bfloat16().cuda()
+
+
+def _call(fn, x, w, residual):
+    """The status word after a call."""
+    (_, S, K), N = x.shape, w.shape[0]
+    out = torch.zeros(1, S, N, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rc = fn(x.data_ptr(), 0, K, K, None, 0, 0, 0, w.data_ptr(), K, 1, S, N, 0, None, None, 0, 0,
+            residual.data_ptr(), 0, N, out.data_ptr(), 0, N, status.data_ptr(),
+            torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+    return int(status.item())
+
+
+def _regular_still_works(x, w, residual):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = binding.linear(x, w, residual=residual, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    R.check(got, R.linear(x, w, residual=residual), "after the timeout")
+
+
+# Problems that run in the split kernel with the channels of a tile over two units
+# or more: single CTAs, pairs over W's rows, pairs over token rows; the sums
+# over the ring (first and last) and in a place of their own.
+FORMS = [(9, 8192, 256), (100, 8192, 2048), (512, 8192, 256), (200, 8192, 4096)]
+
+
+@pytest.mark.parametrize("late", ["some", "all"])
+@pytest.mark.parametrize("S,K,N", FORMS)
+def test_sums_have_arrived_when_an_aborted_cluster_ends(tmp_path, S, K, N, late):
+    """A unit that aborts, and one that waits for it, leave the cluster only
+    after every unit's sums have landed in their shared memory."""
+    skip = "turn != 0" if late == "all" else "turn != 0 || part != 0"
+    landed = ("cluster_wait();  // what this CTA sent has arrived: its shared memory may go",
+              "cluster_wait();\n  if (kC > 1 && !mbar_try_wait_cluster(bar_recv, 0)) "
+              f"atomicMin(status, {NOT_LANDED});\n")
+    fn = _patched(tmp_path, "linear_split_sm103a.cu",
+                  [("commit(bar_empty(s));", f"if ({skip}) commit(bar_empty(s));"), landed, REPORT])
+    x, w, res = _problem(S, K, N)
+    assert _call(fn, x, w, res) == TIMEOUT
+    _regular_still_works(x, w, res)
