@@ -105,6 +105,20 @@ __device__ __forceinline__ void bounded(uint32_t bar, uint32_t parity) {
   }
 }
 
+// After an abort the even CTA of a pair counts no further copies, but the odd
+// one may still have issued some into stages that were free; they complete on
+// the even CTA's barriers in a phase that nobody ends, and the odd CTA, whose
+// accumulators are committed all the same, would not stay for them. The even
+// CTA's producer stays a millisecond (a copy lands within some microseconds, and
+// none is issued later: the MMAs that free stages stop with the abort), and with
+// it the cluster, which no CTA leaves before all have arrived at its last barrier.
+constexpr long long kHoldCycles = 2000000;
+__device__ __forceinline__ void hold_after_abort() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < kHoldCycles) {
+  }
+}
+
 __device__ __forceinline__ void add4(float4 &v, float4 a) {
   v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
 }
@@ -272,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, kForm == kSingle ? 2 : 1)
         else if (turn > 0)
           bounded(bar_full(i), (turn - 1) & 1u);
       }
+    if (kPair && side == 0 && !ok) hold_after_abort();
   } else if (warp == 1 && side == 0) {
     const uint32_t idesc = idesc_bf16_f32(kPair ? 2 * kP : kP, p.Q, 0, 0);
     auto commit = [&](uint32_t bar) {  // arrives in every CTA of the unit

@@ -14,7 +14,7 @@ from tests import block_reference as R
 pytestmark = pytest.mark.gpu
 
 TIMEOUT = -7
-NOT_LANDED = -77  # reported by the copy's kernel, in place of the timeout
+NOT_LANDED, LEFT_EARLY = -77, -78  # reported by the copy's kernel, in place of the timeout
 # the kernels' own report, made not to cover the copy's
 REPORT = ("if (tid == 0 && *abort_flag) atomicExch(status,",
           "if (tid == 0 && *abort_flag) atomicMin(status,")
@@ -101,6 +101,24 @@ def test_sums_have_arrived_when_an_aborted_cluster_ends(tmp_path, S, K, N, late)
               f"atomicMin(status, {NOT_LANDED});\n")
     fn = _patched(tmp_path, "linear_split_sm103a.cu",
                   [("commit(bar_empty(s));", f"if ({skip}) commit(bar_empty(s));"), landed, REPORT])
+    x, w, res = _problem(S, K, N)
+    assert _call(fn, x, w, res) == TIMEOUT
+    _regular_still_works(x, w, res)
+
+
+@pytest.mark.parametrize("S,K,N", [(100, 1536, 2048), (512, 1536, 256)])
+def test_a_pair_stays_for_copies_that_nobody_counts(tmp_path, S, K, N):
+    """The even CTA's producer gives up at its second stage while the odd one
+    goes on: no CTA leaves before the odd one's copies have had a millisecond."""
+    wait = "if (!(ok = mbar_wait_cluster(bar_empty(s), (turn & 1u) ^ 1u, abort_flag))) break;"
+    fn = _patched(tmp_path, "linear_split_sm103a.cu", [
+        ("const uint32_t sbase = smem_addr(base);",
+         "const uint32_t sbase = smem_addr(base);\n  long long gave_up = 0;"),
+        (wait, "if (kPair && side == 0 && ks == k_lo + 1) {\n"
+               "        gave_up = clock64();\n        *abort_flag = 1;\n        ok = false;\n"
+               "        break;\n      }\n      " + wait),
+        (REPORT[0], f"if (gave_up != 0 && clock64() - gave_up < 2000000) "
+                    f"atomicMin(status, {LEFT_EARLY});\n  " + REPORT[1])])
     x, w, res = _problem(S, K, N)
     assert _call(fn, x, w, res) == TIMEOUT
     _regular_still_works(x, w, res)
