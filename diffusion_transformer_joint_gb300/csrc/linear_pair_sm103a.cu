@@ -105,12 +105,6 @@ __device__ __forceinline__ void tile_at(const PairShape &p, int t, int &ft, int 
   rb = first + rem - ft * size;
 }
 
-__device__ __forceinline__ void bounded(uint32_t bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity) && clock64() - t0 < kWaitBudgetCycles) {
-  }
-}
-
 __device__ __forceinline__ void read8(float (&v)[8], const float *p) {
   const float4 a = reinterpret_cast<const float4 *>(p)[0];
   const float4 b = reinterpret_cast<const float4 *>(p)[1];
@@ -207,13 +201,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // stage barriers count both CTAs' copies; the final cluster barrier
     // keeps the odd CTA until then)
     if (crank == 0) {
+      const long long until = clock64() + kWaitBudgetCycles;
       for (int i = 0; i < p.stages; ++i) {
         // the stage's last use, if any, was in this turn or the one before
         if (i < s)
-          bounded(bar(kBarFull + i), turn & 1u);
+          ok &= mbar_settled(bar(kBarFull + i), turn & 1u, until);
         else if (turn > 0)
-          bounded(bar(kBarFull + i), (turn - 1) & 1u);
+          ok &= mbar_settled(bar(kBarFull + i), (turn - 1) & 1u, until);
       }
+      if (!ok) *abort_flag = 1;
     }
   } else if (warp == 1 && crank == 0) {
     // ------------------------------------------------ MMA issuer (even CTA)
@@ -249,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every MMA issued above has finished before TMEM is released
     mma_commit_pair_elect(bar(kBarDrain), 0x1);
-    bounded(bar(kBarDrain), 0);
+    if (!mbar_settled(bar(kBarDrain), 0, clock64() + kWaitBudgetCycles)) *abort_flag = 1;
     __syncwarp();
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
@@ -411,8 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) {
       // residual copies still in flight after an abort, then every output store
+      const long long until = clock64() + kWaitBudgetCycles;
       for (uint32_t j = n_stored; j < n_loaded; ++j)
-        bounded(bar(bar_res + j % kBoxes), (j / kBoxes) & 1u);
+        if (!mbar_settled(bar(bar_res + j % kBoxes), (j / kBoxes) & 1u, until)) *abort_flag = 1;
       bulk_wait_all();
     }
   }

@@ -99,12 +99,6 @@ struct SplitMaps {
   CUtensorMap x, x2, w, w2;
 };
 
-__device__ __forceinline__ void bounded(uint32_t bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait_cluster(bar, parity) && clock64() - t0 < kWaitBudgetCycles) {
-  }
-}
-
 // After an abort the even CTA of a pair counts no further copies, but the odd
 // one may still have issued some into stages that were free; they complete on
 // the even CTA's barriers in a phase that nobody ends, and the odd CTA, whose
@@ -278,15 +272,20 @@ __global__ void __launch_bounds__(kThreads, kForm == kSingle ? 2 : 1)
     }
     // every copy of the unit has landed before its CTAs exit (the final cluster
     // barrier keeps the odd CTA until then)
-    if (side == 0)
+    if (side == 0) {
+      const long long until = clock64() + kWaitBudgetCycles;
       for (int i = 0; i < p.stages; ++i) {
         // the stage's last use, if any, was in this turn or the one before
         if (i < s)
-          bounded(bar_full(i), turn & 1u);
+          ok &= mbar_settled(bar_full(i), turn & 1u, until);
         else if (turn > 0)
-          bounded(bar_full(i), (turn - 1) & 1u);
+          ok &= mbar_settled(bar_full(i), (turn - 1) & 1u, until);
       }
-    if (kPair && side == 0 && !ok) hold_after_abort();
+      if (!ok) {
+        *abort_flag = 1;
+        if constexpr (kPair) hold_after_abort();
+      }
+    }
   } else if (warp == 1 && side == 0) {
     const uint32_t idesc = idesc_bf16_f32(kPair ? 2 * kP : kP, p.Q, 0, 0);
     auto commit = [&](uint32_t bar) {  // arrives in every CTA of the unit
@@ -333,8 +332,9 @@ __global__ void __launch_bounds__(kThreads, kForm == kSingle ? 2 : 1)
   }
   __syncwarp();
   // every MMA of the unit has finished: the accumulator is complete and the
-  // stages free (an aborted unit's MMAs in flight are waited for too)
-  bounded(bar_acc, 0);
+  // stages free. An aborted unit's MMAs in flight are waited for too: its issuer
+  // commits them when its own wait has run out, so that this one is longer.
+  if (!mbar_settled(bar_acc, 0, clock64() + 3 * kWaitBudgetCycles)) *abort_flag = 1;
   tc_fence_after_sync();
   __syncthreads();
   {
@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(kThreads, kForm == kSingle ? 2 : 1)
     __syncwarp();
     // An abort does not end this wait: every unit sends its rows, an aborted one
     // too, and they must have arrived before this CTA lets the cluster go. The
-    // last unit may have waited for a stage and then for its copies, a budget
-    // each, since this one was done.
+    // last unit may have waited for its accumulators for three budgets since this
+    // one was done.
     if (!mbar_try_wait_cluster(bar_recv, 0) &&
         !mbar_settled(bar_recv, 0, clock64() + 4 * kWaitBudgetCycles))
       *abort_flag = 1;

@@ -122,3 +122,19 @@ def test_a_pair_stays_for_copies_that_nobody_counts(tmp_path, S, K, N):
     x, w, res = _problem(S, K, N)
     assert _call(fn, x, w, res) == TIMEOUT
     _regular_still_works(x, w, res)
+
+
+SPLIT_ACC = ("linear_split_sm103a.cu", "commit(bar_acc);", "if (part != 0) commit(bar_acc);")
+PAIR_DRAIN = ("linear_pair_sm103a.cu", "mma_commit_pair_elect(bar(kBarDrain), 0x1);",
+              "if (cid != 0) mma_commit_pair_elect(bar(kBarDrain), 0x1);")
+
+
+@pytest.mark.parametrize("patch,S,K,N", [(SPLIT_ACC, 9, 8192, 256), (SPLIT_ACC, 512, 8192, 256),
+                                         (PAIR_DRAIN, 2600, 64, 4096)])
+def test_the_last_waits_report_too(tmp_path, patch, S, K, N):
+    """The waits for a unit's accumulators and for the last MMAs, which an abort
+    does not cut short, set the status word when they run out."""
+    fn = _patched(tmp_path, patch[0], [patch[1:]])
+    x, w, res = _problem(S, K, N)
+    assert _call(fn, x, w, res) == TIMEOUT
+    _regular_still_works(x, w, res)
