@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t turn = 0;
     int lt = 0;
     bool ok = true;
+    grid_dep_wait();  // the budget of the first stage's wait begins with its copy
     for (int t = cid; ok && t < p.n_tiles; t += ncl, ++lt) {
       const int buf = lt & 1;
       const uint32_t acc_par = ((static_cast<uint32_t>(lt) >> 1) & 1u) ^ 1u;
