@@ -32,7 +32,7 @@ EXPORTS = ("flux_rope_tables", "flux_rope_tables_packed", "flux_joint_rope_atten
            "flux_joint_rope_attention_cached_workspace", "flux_joint_rope_attention_cached",
            "flux_joint_qknorm_rope_attention_extract", "flux_joint_qknorm_rope_attention_cached",
            "flux_qkv_mlp_proj", "flux_linear", "flux_modulated_norm", "flux_query_status",
-           "flux_status_string")
+           "flux_status_word", "flux_take_status", "flux_status_string")
 
 
 class FluxError(RuntimeError):
@@ -129,6 +129,10 @@ def load(path: str | None = None):
             lib.flux_modulated_norm.restype = I32
             lib.flux_query_status.argtypes = [V, V]
             lib.flux_query_status.restype = I32
+            lib.flux_status_word.argtypes = [V]
+            lib.flux_status_word.restype = I32
+            lib.flux_take_status.argtypes = [V]
+            lib.flux_take_status.restype = I32
             lib.flux_status_string.argtypes = [I32]
             lib.flux_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -585,8 +589,8 @@ def attention_cached(q, k, v, txt_ids, img_ids, cache_k, cache_v, axes_dims=AXES
 def qkv_mlp_proj(x, w, H, mlp=None, q=None, k=None, v=None, act=None, status=None,
                  stream=None):
     """Fused single-stream input projection: x [..., dim] and w [3 H 128 + 2 mlp, dim]
-    bf16 -> (q, k, v [..., H, 128], act [..., mlp]); status (int32 [1], cleared
-    here when allocated) receives a device timeout."""
+    bf16 -> (q, k, v [..., H, 128], act [..., mlp]); status (int32 [1]) receives a
+    device timeout, without it the device's own word (take_status)."""
     import torch
 
     lib = load()
@@ -609,16 +613,18 @@ def qkv_mlp_proj(x, w, H, mlp=None, q=None, k=None, v=None, act=None, status=Non
     v = torch.empty(lead + (H, 128), dtype=torch.bfloat16, device=dev) if v is None else v
     if act is None:
         act = torch.empty(lead + (mlp,), dtype=torch.bfloat16, device=dev)
-    if status is None:
-        status = torch.zeros(1, dtype=torch.int32, device=dev)
     for name, t in (("q", q), ("k", k), ("v", v), ("act", act)):
         _need_cuda(name, t, torch.bfloat16)
     for name, t in (("q", q), ("k", k), ("v", v)):
         _need_shape(name, t, lead + (H, 128))
     _need_shape("act", act, lead + (mlp,))
-    _need_cuda("status", status, torch.int32)
+    if status is None:
+        sp = _own_status(lib, torch.cuda.current_device())
+    else:
+        _need_cuda("status", status, torch.int32)
+        sp = _ptr(status)
     rc = lib.flux_qkv_mlp_proj(_ptr(x), _ptr(w), M, dim, int(H), 128, int(mlp), _ptr(q), _ptr(k),
-                               _ptr(v), _ptr(act) if mlp > 0 else None, _ptr(status),
+                               _ptr(v), _ptr(act) if mlp > 0 else None, sp,
                                _stream_handle(stream))
     if rc != 0:
         raise FluxError("flux_qkv_mlp_proj", rc, lib)
@@ -715,8 +721,9 @@ def linear(x, w, x2=None, bias=None, act=None, gate=None, residual=None, out=Non
     and gate [N] or [B, N] are both bf16 or both fp32; residual and ``out`` are
     bf16 [B, S, N] (``out=residual`` updates a stream in place). Token tensors
     and w may have strides between rows and batch elements (views of a joint
-    sequence, of a wider buffer or of w's columns). ``status`` (int32 [1],
-    cleared here when allocated) receives a device timeout. Returns out.
+    sequence, of a wider buffer or of w's columns). ``status`` (int32 [1])
+    receives a device timeout, without it the device's own word (take_status).
+    Returns out.
     """
     import torch
 
@@ -757,11 +764,13 @@ def linear(x, w, x2=None, bias=None, act=None, gate=None, residual=None, out=Non
         out = _allocate(stream, torch.empty, shape, dtype=bf16, device=x.device)
     op, ob, orow = _token_rows("out", out, shape, bf16, dev)
     if status is None:
-        status = _allocate(stream, torch.zeros, 1, dtype=torch.int32, device=x.device)
+        sp = _own_words.get(dev) or _own_status(lib, dev)
     elif status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != dev:
         raise ValueError(f"status must hold one int32 on cuda:{dev}")
+    else:
+        sp = status.data_ptr()
     rc = lib.flux_linear(xp, xb, xr, K, x2p, x2b, x2r, K2, wp, wr, B, S, N, code, bp, gp, gb,
-                         vec_f32, rp, rb, rr, op, ob, orow, status.data_ptr(), handle)
+                         vec_f32, rp, rb, rr, op, ob, orow, sp, handle)
     if rc != 0:
         raise FluxError("flux_linear", rc, lib)
     return out
@@ -819,6 +828,28 @@ def modulated_norm(x, scale=None, shift=None, y=None, gate=None, norm="layer", e
     if rc != 0:
         raise FluxError("flux_modulated_norm", rc, lib)
     return out if y is None else (out, x_out)
+
+
+_own_words = {}  # address of the library's own status word, by device
+
+
+def _own_status(lib, dev):
+    """The library's own status word on `dev`, the current device."""
+    if dev not in _own_words:
+        word = ctypes.c_void_p()
+        rc = lib.flux_status_word(ctypes.byref(word))
+        if rc != 0:
+            raise FluxError("flux_status_word", rc, lib)
+        _own_words[dev] = word.value
+    return _own_words[dev]
+
+
+def take_status(stream=None) -> int:
+    """Synchronise and return the current device's own status word, which calls
+    without ``status`` report to (0, or FLUX_ERR_DEVICE_TIMEOUT if a bounded wait
+    of one of them ran out since it was last taken); clears it."""
+    lib = load()
+    return int(lib.flux_take_status(_stream_handle(stream)))
 
 
 def query_status(workspace, stream=None) -> int:

@@ -2,6 +2,8 @@
 // declared in include/flux_attn.h: argument checks and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "flux_internal.h"
 #include "linear_common.cuh"
 
@@ -105,6 +107,25 @@ Rows vec_rows(const void *p, int64_t B, int64_t width, int64_t bs, int f32) {
 }
 
 constexpr int64_t kMaxTokens = int64_t{1} << 30;
+
+// The library's own status word, one per device that loads the library. The
+// host's name for it is no device address: own_status_word looks that up.
+static __device__ int32_t g_status;
+
+int32_t *own_status_word() {
+  static std::atomic<void *> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  void *p = cached[dev].load(std::memory_order_relaxed);
+  if (p == nullptr) {
+    if (cudaGetSymbolAddress(&p, g_status) != cudaSuccess) {
+      (void)cudaGetLastError();  // not to surface in a later call
+      return nullptr;
+    }
+    cached[dev].store(p, std::memory_order_relaxed);
+  }
+  return static_cast<int32_t *>(p);
+}
 
 // Batch elements that follow one another at the token stride are one run of
 // tokens.
@@ -228,6 +249,23 @@ int flux_modulated_norm(const void *x, int64_t x_bs, int64_t x_rs, int stream_f3
   return flux::launch_modulated_norm(q, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? FLUX_OK
              : FLUX_ERR_CUDA;
+}
+
+int flux_status_word(int32_t **status) {
+  if (status == nullptr) return FLUX_ERR_NULL;
+  const int dc = flux::check_device();
+  if (dc != FLUX_OK) return dc;
+  *status = own_status_word();
+  return *status != nullptr ? FLUX_OK : FLUX_ERR_CUDA;
+}
+
+int flux_take_status(void *stream) {
+  int32_t *word = nullptr;
+  const int rc = flux_status_word(&word);
+  if (rc != FLUX_OK) return rc;
+  const int status = flux_query_status(word, stream);
+  if (status != FLUX_OK && cudaMemset(word, 0, sizeof(*word)) != cudaSuccess) return FLUX_ERR_CUDA;
+  return status;
 }
 
 }  // extern "C"

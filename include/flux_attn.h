@@ -44,8 +44,9 @@
  *   - Device-side failures (a bounded wait inside a kernel that ran out)
  *     never trap: the kernel records FLUX_ERR_DEVICE_TIMEOUT in a status word
  *     and returns. Entry points with a workspace keep the word at its start
- *     (read it with flux_query_status()); the tabled attention and the
- *     projection take a caller-owned device int32 instead.
+ *     (read it with flux_query_status()); the tabled attention, the projection
+ *     and the linear layer take a device int32 instead, the caller's or the
+ *     library's own (flux_status_word()).
  */
 #ifndef FLUX_ATTN_H
 #define FLUX_ATTN_H
@@ -563,6 +564,19 @@ int flux_joint_rope_attention_noalloc_status(void *stream);
  * synchronisation or the copy fails.
  */
 int flux_query_status(const void *workspace, void *stream);
+
+/*
+ * flux_status_word: *status becomes the address, on the current device, of a
+ * status word of the library's own, for callers that keep none: one word per
+ * device, 0 until a bounded wait of a call that was given it runs out, shared by
+ * streams, threads and captured graphs (a kernel writes it only then), valid
+ * until the process exits.
+ * flux_take_status: synchronises `stream`, returns that word and, where it is
+ * not FLUX_OK, clears it. Calls still under way on other streams are not waited
+ * for. FLUX_ERR_CUDA when a CUDA call fails.
+ */
+int flux_status_word(int32_t **status);
+int flux_take_status(void *stream);
 
 /* flux_status_string: static description of a status code (never NULL). */
 const char *flux_status_string(int status);
