@@ -133,6 +133,15 @@ bool joins(const Rows &t) { return t.p == nullptr || t.B == 1 || t.bs == t.S * t
 
 }  // namespace
 
+// With few tokens most rows of linear_pair's tiles would be empty, and its
+// estimate is not fitted there.
+flux::LinearPlan flux::plan_linear(const LinearProblem &q, int act, int sms) {
+  LinearPlan p{true, plan_split(q, act, sms), {0, 2e30}};
+  if (q.B * q.S >= 128) p.pair = plan_pair(q, act, sms);
+  p.use_split = p.split.ns < p.pair.ns;
+  return p;
+}
+
 extern "C" {
 
 int flux_linear(const void *x, int64_t x_bs, int64_t x_rs, int K, const void *x2, int64_t x2_bs,
@@ -184,17 +193,13 @@ int flux_linear(const void *x, int64_t x_bs, int64_t x_rs, int K, const void *x2
   if (q.B == 1) {  // (a batch stride that nothing looks at, but the tensor maps take)
     q.x_bs = q.x_rs * q.S, q.x2_bs = q.x2_rs * q.S, q.r_bs = q.r_rs * q.S, q.o_bs = q.o_rs * q.S;
   }
-  // the form with the smaller estimate; with few tokens most rows of linear_pair's
-  // tiles would be empty, and its estimate is not fitted there
   const int sms = flux::sm_count_current_device();
   if (sms < 1) return FLUX_ERR_CUDA;
-  const flux::SplitPlan split = flux::plan_split(q, act, sms);
-  flux::PairPlan pair{0, 2e30};
-  if (q.B * q.S >= 128) pair = flux::plan_pair(q, act, sms);
+  const flux::LinearPlan plan = flux::plan_linear(q, act, sms);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = split.ns < pair.ns
-                            ? flux::launch_linear_split(q, split, epi, act, status, st)
-                            : flux::launch_linear_pair(q, pair, epi, act, status, st);
+  const cudaError_t e = plan.use_split
+                            ? flux::launch_linear_split(q, plan.split, epi, act, status, st)
+                            : flux::launch_linear_pair(q, plan.pair, epi, act, status, st);
   return e == cudaSuccess ? FLUX_OK : FLUX_ERR_CUDA;
 }
 

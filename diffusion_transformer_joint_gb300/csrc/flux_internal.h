@@ -165,6 +165,14 @@ struct PairPlan {
 SplitPlan plan_split(const LinearProblem &q, int act, int sms);
 PairPlan plan_pair(const LinearProblem &q, int act, int sms);
 
+// The form with the smaller estimate: split, or else pair.
+struct LinearPlan {
+  bool use_split;
+  SplitPlan split;
+  PairPlan pair;
+};
+LinearPlan plan_linear(const LinearProblem &q, int act, int sms);
+
 // The two kernels behind flux_linear (act: a flux_activation).
 cudaError_t launch_linear_pair(const LinearProblem &q, const PairPlan &plan,
                                const LinearEpilogue &epi, int act, int *status,

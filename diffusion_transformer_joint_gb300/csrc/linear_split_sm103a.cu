@@ -581,7 +581,8 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
   switch (plan.form) {
     case kSingle: return launch<kAct, kSingle>(q, plan, epi, status, stream);
     case kPairW: return launch<kAct, kPairW>(q, plan, epi, status, stream);
-    default: return launch<kAct, kPairX>(q, plan, epi, status, stream);
+    case kPairX: return launch<kAct, kPairX>(q, plan, epi, status, stream);
+    default: return cudaErrorInvalidValue;
   }
 }
 
@@ -610,7 +611,7 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
   };
   static constexpr Costs kPairCosts = {0.0, 4100.0, 240.0, 0.0, 330.0, 0.056, 23000.0, 123.0};
   static constexpr Costs kSingleCosts = {1275.0, 4720.0, -2210.0, 16.0, 158.0, 0.046, 7860.0, 92.0};
-  SplitPlan best{kPairX, false, 32, 1, 2, 1e30};
+  SplitPlan best{-1, false, 0, 0, 0, 1e30};  // no form yet
   auto consider = [&](int form, int Q) {
     const bool single = form == kSingle;
     const int64_t feats = (form == kPairX ? Q : single ? kP : 2 * kP) / (glu ? 2 : 1);
@@ -648,7 +649,10 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
   const int64_t rows8 = q.B * ((q.S + 7) / 8 * 8), rows16 = q.B * ((q.S + 15) / 16 * 16);
   if (rows8 <= 64) consider(kSingle, static_cast<int>((rows8 + 15) / 16 * 16));
   if (rows16 <= 256) consider(kPairW, static_cast<int>((rows16 + 31) / 32 * 32));
-  if (q.B * q.S >= 64)  // fewer tokens would fill less than a quarter of P
+  // Fewer tokens would fill less than a quarter of P; but of many batch elements
+  // that do not follow one another, each rounded up, the tokens may be too many
+  // columns for either form above.
+  if (q.B * q.S >= 64 || best.form < 0)
     for (int Q = 32; Q <= 256; Q += 32) consider(kPairX, Q);
   return best;
 }
