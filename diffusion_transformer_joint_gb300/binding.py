@@ -737,6 +737,8 @@ def linear(x, w, x2=None, bias=None, act=None, gate=None, residual=None, out=Non
         raise ValueError(f"act must be one of {list(ACTIVATIONS)}, got {act!r}")
     B, S, K = shape if len(shape) == 3 else (1, *shape)
     K2 = 0 if x2 is None else x2.shape[-1]
+    if B > 0x7FFFFFFF or K > 0x7FFFFFFF or K2 > 0x7FFFFFFF:
+        raise ValueError(f"batch and channels must be below 2^31, got {B}, {K}, {K2}")
     xp, xb, xr = _token_rows("x", x, shape, bf16, dev)
     if w.dim() != 2 or w.shape[1] != K + K2:
         raise ValueError(f"w must be [rows, {K + K2}], got {tuple(w.shape)}")
@@ -800,6 +802,8 @@ def modulated_norm(x, scale=None, shift=None, y=None, gate=None, norm="layer", e
     if kind is None:
         raise ValueError(f"norm must be one of {list(NORMS)}, got {norm!r}")
     B, S, dim = shape if len(shape) == 3 else (1, *shape)
+    if B > 0x7FFFFFFF or dim > 0x7FFFFFFF:
+        raise ValueError(f"batch and channels must be below 2^31, got {B}, {dim}")
     xp, xb, xr = _token_rows("x", x, shape, dtype, dev)
     sp = fp = gp = yp = op = None
     sb = fb = gb = yb = yr = ob = orow = vec_f32 = 0
