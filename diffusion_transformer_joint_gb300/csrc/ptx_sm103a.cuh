@@ -161,11 +161,8 @@ __device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int
       "r"(src), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// Wait until at most three (one) of this thread's committed store groups
-// still read shared memory.
-__device__ __forceinline__ void bulk_wait_read_3() {
-  asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
-}
+// Wait until at most one of this thread's committed store groups still reads
+// shared memory.
 __device__ __forceinline__ void bulk_wait_read_1() {
   asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
@@ -321,12 +318,6 @@ __device__ __forceinline__ uint32_t cluster_id_x() {
 __device__ __forceinline__ uint32_t cluster_count_x() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
-  return r;
-}
-// CTAs in this CTA's cluster.
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
 // Every thread of the cluster's CTAs arrives, then waits for all.
@@ -667,17 +658,6 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
 
 __device__ __forceinline__ void st_shared_b32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-// A 16-byte load of data that is read once and may be overwritten later by
-// this kernel: not the read-only path, not kept in L1.
-__device__ __forceinline__ uint4 ld_global_stream_v4(const void *p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
