@@ -26,8 +26,10 @@ struct LinearEpilogue {
 
 // act(y) in fp32. SiLU y / (1 + e^-y); GELU in its tanh form, of which
 // 0.5 (1 + tanh u) = 1 / (1 + e^-2u) needs one exponential. The fast division
-// is off by two fp32 steps (and gives 0 where the divisor passes 2^126, as the
-// quotient's bf16 does): an epilogue with the exact one took twice as long.
+// is off by two fp32 steps, and gives 0 where the divisor passes 2^126: SiLU is
+// 0 below y of about -87.3, where its value, which bf16 could still hold down to
+// -97 or so, is under 1.1e-36 in magnitude; GELU's is far smaller there. An
+// epilogue with the exact division took twice as long.
 template <int kAct>
 __device__ __forceinline__ float activate(float y) {
   if constexpr (kAct == FLUX_ACT_SILU) {
@@ -93,8 +95,9 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // What the plans' estimates (ns) share: an SM takes in about 112 bytes per ns;
 // a stage's 64 channels are four MMAs of N / 2 cycles, about N ns. Fitted, like
 // the constants beside them, to the times of every form at 103 problems of 1 to
-// 4608 rows: the form that the estimates pick takes 1.01 times the best one's
-// time (geometric mean; at most 1.17).
+// 4608 rows, 256 to 16384 channels and 128 to 24576 features: the form that the
+// estimates pick takes 1.006 times the best one's time there (geometric mean; at
+// most 1.17). Beyond those sizes the estimates only extrapolate.
 constexpr double kBytesPerNs = 112.0;
 inline double stage_ns(double bytes, int n) {
   return bytes / kBytesPerNs > n ? bytes / kBytesPerNs : n;

@@ -9,7 +9,7 @@
 // columns are tn output features; for SwiGLU tn/2 gate features and the
 // linear features of the same tn/2 outputs, so that the epilogue holds both
 // factors of what it writes. tn is a launch parameter (the MMA's N is part of
-// its instruction descriptor), chosen by pick_tile.
+// its instruction descriptor), chosen by plan_pair.
 //
 // CTA pairs (clusters of two, one CTA per SM): one M256 N=tn K16 MMA per 16
 // channels, issued by the even CTA and reading both CTAs' shared memory. Each

@@ -603,9 +603,12 @@ SplitPlan plan_split(const LinearProblem &q, int act, int sms) {
                                   (q.residual != nullptr ? 2 : 1));
   static constexpr int kResident[2][9] = {{0, 152, 152, 0, 144, 0, 138, 0, 120},    // an SM each
                                           {0, 304, 304, 291, 296, 0, 276, 0, 288}};  // half an SM
-  // ns: to refill a ring (what a pair's brings hides it), a wave, a call, a row
-  // of Q, to join sums, to finish one; bytes per ns: of the memory, of sums
-  // between CTAs
+  // Coefficients of a regression over the 103 problems, each named for what its
+  // term grows with; they make up for one another and are no measurements. In ns:
+  // per refill of a ring (what a pair's ring brings hides it), wave, call, row of
+  // Q, joining of sums, sum finished. In bytes per ns: hbm for all bytes (the
+  // memory has 6770; a pair's stages, waves and sums account for its times without
+  // that bound), send for the sums sent (bulk copies reach about 30 per SM).
   struct Costs {
     double refill, wave, call, row, join, finish, hbm, send;
   };
