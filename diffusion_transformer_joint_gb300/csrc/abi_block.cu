@@ -269,7 +269,12 @@ int flux_take_status(void *stream) {
   const int rc = flux_status_word(&word);
   if (rc != FLUX_OK) return rc;
   const int status = flux_query_status(word, stream);
-  if (status != FLUX_OK && cudaMemset(word, 0, sizeof(*word)) != cudaSuccess) return FLUX_ERR_CUDA;
+  if (status == FLUX_OK) return status;
+  // cleared before a later call of the stream can report again
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (cudaMemsetAsync(word, 0, sizeof(*word), st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return FLUX_ERR_CUDA;
   return status;
 }
 
