@@ -69,9 +69,12 @@ constexpr int max_units(int form) { return form == kSingle ? kMaxUnits : kMaxUni
 constexpr int kThreads = 512;
 constexpr uint32_t kSmemAll = 232448;   // a pair's CTAs: one per SM
 constexpr uint32_t kSmemHalf = 114688;  // single CTAs: two per SM
-// A pair's CTA takes no less: beside it an SM has no room for another CTA that
-// allocates TMEM (a single one's ring takes 96 KB or more).
-constexpr uint32_t kSmemPair = 147456;
+// CTAs take no less, whatever their plan needs: beside a pair's CTA an SM (228 KB,
+// of which the system takes 1 KB per CTA) has no room for another that allocates
+// TMEM.
+constexpr uint32_t kSmemPair = 147456, kSmemSingle = 98304;
+constexpr uint32_t kSmemSm = 233472 - 2 * 1024;  // for two CTAs
+static_assert(2 * kSmemPair > kSmemSm && kSmemPair + kSmemSingle > kSmemSm, "a pair's SM");
 constexpr uint32_t kTailBytes = 256;    // barriers and flags
 // A ring that sums may have a place of their own beside: with less on its way
 // than about 1.5 us of what an SM takes in, the stages wait for the memory.
@@ -523,7 +526,7 @@ cudaError_t launch(const LinearProblem &q, const SplitPlan &plan, const LinearEp
   p.recv = plan.early ? std::max(ring, own) : own;
   p.tail = std::max(ring, p.recv + recv_bytes(kForm, p.Q, kC));
   const uint32_t need = p.tail + kTailBytes;
-  const uint32_t smem = kForm == kSingle ? need : std::max(need, kSmemPair);
+  const uint32_t smem = std::max(need, kForm == kSingle ? kSmemSingle : kSmemPair);
   if (smem > (kForm == kSingle ? kSmemHalf : kSmemAll)) return cudaErrorInvalidValue;
   const uint32_t w_box = static_cast<uint32_t>(kForm == kPairX ? p.Q / 2 : p.feats);
   const uint32_t x_box = static_cast<uint32_t>(kForm == kPairX ? kP : p.Sh);
