@@ -429,10 +429,11 @@ typedef enum {
  *   y = [x | x2] W^T + bias  (fp32 accumulation),
  *   out = residual + gate * act(y), rounded once to bf16 (nearest even).
  *
- *   x          device, bf16 [B, S, K]; K a multiple of 8.
+ *   x          device, bf16 [B, S, K]; K a multiple of 8, at most 2^28.
  *   x2, K2     more input channels, bf16 [B, S, K2], after those of x (the
  *              single-stream block's [attention | MLP] without the
- *              concatenation); K2 a multiple of 8, 0: none (x2 may be NULL).
+ *              concatenation); K2 a multiple of 8, at most 2^28, 0: none (x2 may
+ *              be NULL).
  *   w, w_rs    device, bf16 [N, K + K2] with row stride w_rs (a linear layer's
  *              weight, or a range of its columns); for FLUX_ACT_SWIGLU
  *              [2 N, K + K2], the N gate rows, then the N linear rows.
@@ -442,8 +443,9 @@ typedef enum {
  *   gate       [B, N] at batch stride gate_bs, or NULL (1).
  *   residual   bf16 [B, S, N] or NULL (0); may be `out` itself.
  *   out        bf16 [B, S, N]; written, not read (unless it is the residual).
- *   status     device int32 word; the kernel writes FLUX_ERR_DEVICE_TIMEOUT
- *              there if a bounded wait runs out and never writes it otherwise.
+ *   status     device int32 word (flux_status_word() gives one); the kernel writes
+ *              FLUX_ERR_DEVICE_TIMEOUT there if a bounded wait runs out and never
+ *              writes it otherwise.
  * The sums are added in an order that depends on the sizes only: the same call
  * gives the same bits every time.
  * Returns FLUX_OK when the kernel was enqueued, else a negative status.
