@@ -27,9 +27,9 @@ struct LinearEpilogue {
 // act(y) in fp32. SiLU y / (1 + e^-y); GELU in its tanh form, of which
 // 0.5 (1 + tanh u) = 1 / (1 + e^-2u) needs one exponential. The fast division
 // is off by two fp32 steps, and gives 0 where the divisor passes 2^126: SiLU is
-// 0 below y of about -87.3, where its value, which bf16 could still hold down to
-// -97 or so, is under 1.1e-36 in magnitude; GELU's is far smaller there. An
-// epilogue with the exact division took twice as long.
+// 0 below y of about -87.3, GELU below -10, where their values, some of which
+// bf16 could still hold, are under 1.1e-36 and 1.2e-37 in magnitude. An epilogue
+// with the exact division took twice as long.
 template <int kAct>
 __device__ __forceinline__ float activate(float y) {
   if constexpr (kAct == FLUX_ACT_SILU) {
