@@ -10,10 +10,12 @@ pytestmark = pytest.mark.gpu
 FAR = 2 ** 32 + 64
 
 
-@pytest.fixture(scope="module", autouse=True)
+@pytest.fixture(autouse=True)
 def _lib():
     build.build()
     binding.load()
+    yield
+    torch.cuda.empty_cache()
 
 
 def test_norm_refuses_channels_past_an_int():
