@@ -161,7 +161,9 @@ def _groups(x, rows):
 def _to_e4m3(x, rows):
     """(e4m3 values, fp32 scales per group), in fp32."""
     top, wide = _groups(x.float(), rows)
-    return (x.float() * (TOP / wide)).to(torch.float8_e4m3fn), top / TOP
+    # (a number over a tensor would be its reciprocal's multiple, rounded twice)
+    q = x.float() * (torch.full_like(wide, TOP) / wide)
+    return q.to(torch.float8_e4m3fn), top / TOP
 
 
 def prepare(case, seed):
