@@ -31,8 +31,9 @@ EXPORTS = ("flux_rope_tables", "flux_rope_tables_packed", "flux_joint_rope_atten
            "flux_joint_rope_attention_extract_workspace", "flux_joint_rope_attention_extract",
            "flux_joint_rope_attention_cached_workspace", "flux_joint_rope_attention_cached",
            "flux_joint_qknorm_rope_attention_extract", "flux_joint_qknorm_rope_attention_cached",
-           "flux_qkv_mlp_proj", "flux_linear", "flux_modulated_norm", "flux_query_status",
-           "flux_status_word", "flux_take_status", "flux_status_string")
+           "flux_qkv_mlp_proj", "flux_linear", "flux_modulated_norm", "flux_quantize_fp8",
+           "flux_linear_fp8", "flux_query_status", "flux_status_word", "flux_take_status",
+           "flux_status_string")
 
 
 class FluxError(RuntimeError):
@@ -127,6 +128,13 @@ def load(path: str | None = None):
                                                 I64, I32, I32, I64, I32, I32, F, V, I64, I64, V,
                                                 I64, I64, V]
             lib.flux_modulated_norm.restype = I32
+            lib.flux_quantize_fp8.argtypes = [V, I64, I64, I32, I32, I64, I32, I32, V, I64, I64, V,
+                                              I64, I64, I64, V]
+            lib.flux_quantize_fp8.restype = I32
+            lib.flux_linear_fp8.argtypes = [V, I64, I64, V, I64, I64, I64, V, I64, V, I64, I64,
+                                            I32, I64, I32, I64, I32, V, V, I64, I32, V, I64, I64,
+                                            V, I64, I64, V, V]
+            lib.flux_linear_fp8.restype = I32
             lib.flux_query_status.argtypes = [V, V]
             lib.flux_query_status.restype = I32
             lib.flux_status_word.argtypes = [V]
@@ -832,6 +840,136 @@ def modulated_norm(x, scale=None, shift=None, y=None, gate=None, norm="layer", e
     if rc != 0:
         raise FluxError("flux_modulated_norm", rc, lib)
     return out if y is None else (out, x_out)
+
+
+def _scales(name, t, shape, dev):
+    """(address, strides of a group's scales [..., rows, groups]); any strides."""
+    import torch
+
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be float32, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    st = t.stride()
+    return (t.data_ptr(), *st) if len(st) == 3 else (t.data_ptr(), 0, *st)
+
+
+def quantize_fp8(x, rows=1, out=None, scale=None, stream=None):
+    """Rows or a weight in e4m3 with an fp32 scale per group: scale = t / 448 and
+    q = e4m3(x * (448 / t)), t the group's largest magnitude.
+
+    x: bf16 or fp32 CUDA [B, S, K] (or [S, K]), K a multiple of 16, with strides
+    between rows and batch elements as for linear. rows: 1, a group is 128
+    channels of a row (activations), or 128, it is 128 x 128 of x [N, K]
+    (weights). ``out`` is torch.float8_e4m3fn of x's shape; ``scale`` [B, S,
+    ceil(K / 128)] ([S, ..]; [ceil(N / 128), ..]) of any strides, made with the
+    tokens beside one another. Returns (out, scale).
+    """
+    import torch
+
+    lib = _lib or load()
+    dev, handle = _stream_of(x, stream)
+    e4m3, shape, dtype = torch.float8_e4m3fn, x.shape, x.dtype
+    if len(shape) not in (2, 3):
+        raise ValueError(f"x must be [B, S, K] or [S, K], got {tuple(shape)}")
+    if dtype != torch.bfloat16 and dtype != torch.float32:
+        raise ValueError(f"x must be bfloat16 or float32, got {dtype}")
+    if rows not in (1, 128) or (rows == 128 and len(shape) != 2):
+        raise ValueError(f"rows must be 1, or 128 for x [N, K]; got {rows}, {tuple(shape)}")
+    B, S, K = shape if len(shape) == 3 else (1, *shape)
+    if B > 0x7FFFFFFF or K > 0x7FFFFFFF:
+        raise ValueError(f"batch and channels must be below 2^31, got {B}, {K}")
+    xp, xb, xr = _token_rows("x", x, shape, dtype, dev)
+    groups = (K + 127) // 128
+    if out is None:
+        out = _allocate(stream, torch.empty, shape, dtype=e4m3, device=x.device)
+    qp, qb, qr = _token_rows("out", out, shape, e4m3, dev)
+    lead = shape[:-1] if rows == 1 else ((S + 127) // 128,)
+    if scale is None:
+        if rows == 1:
+            scale = _allocate(stream, torch.empty_strided, (*lead, groups),
+                              ((S, 1, B * S) if len(shape) == 3 else (1, S)),
+                              dtype=torch.float32, device=x.device)
+        else:
+            scale = _allocate(stream, torch.empty, (*lead, groups), dtype=torch.float32,
+                              device=x.device)
+    sp, sb, sr, sk = _scales("scale", scale, (*lead, groups), dev)
+    rc = lib.flux_quantize_fp8(xp, xb, xr, int(dtype == torch.float32), B, S, K, rows, qp, qb, qr,
+                               sp, sb, sr, sk, handle)
+    if rc != 0:
+        raise FluxError("flux_quantize_fp8", rc, lib)
+    return out, scale
+
+
+def linear_fp8(x, x_scale, w, w_scale, bias=None, act=None, gate=None, residual=None, out=None,
+               status=None, stream=None):
+    """A linear layer in 8 bits: residual + gate * act(x W^T + bias), x and W e4m3
+    values times their groups' scales (quantize_fp8).
+
+    x: torch.float8_e4m3fn CUDA [B, S, K] (or [S, K]), x_scale fp32 [B, S,
+    ceil(K / 128)]; w [N, K] ([2 N, K] for act "swiglu", N a multiple of 128) with
+    w_scale [ceil(rows / 128), ceil(K / 128)]. Scales may have any strides. Other
+    arguments and the result as for linear.
+    """
+    import torch
+
+    lib = _lib or load()
+    dev, handle = _stream_of(x, stream)
+    bf16, e4m3, shape = torch.bfloat16, torch.float8_e4m3fn, x.shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"x must be [B, S, K] or [S, K], got {tuple(shape)}")
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {list(ACTIVATIONS)}, got {act!r}")
+    B, S, K = shape if len(shape) == 3 else (1, *shape)
+    if B > 0x7FFFFFFF or K > 0x7FFFFFFF:
+        raise ValueError(f"batch and channels must be below 2^31, got {B}, {K}")
+    groups = (K + 127) // 128
+    xp, xb, xr = _token_rows("x", x, shape, e4m3, dev)
+    xsp, xsb, xsr, xsk = _scales("x_scale", x_scale, (*shape[:-1], groups), dev)
+    if w.dim() != 2 or w.shape[1] != K:
+        raise ValueError(f"w must be [rows, {K}], got {tuple(w.shape)}")
+    wp, _, wr = _token_rows("w", w, w.shape, e4m3, dev)
+    rows = N = w.shape[0]
+    wsp, _, wsr, wsk = _scales("w_scale", w_scale, ((rows + 127) // 128, groups), dev)
+    if act == "swiglu":
+        if rows % 2:
+            raise ValueError(f"w must have two equal halves of rows, got {rows}")
+        N = rows // 2
+    shape = (*shape[:-1], N)
+    bp = gp = rp = None
+    gb = vec_f32 = rb = rr = 0
+    if residual is not None:
+        rp, rb, rr = _token_rows("residual", residual, shape, bf16, dev)
+    if bias is not None or gate is not None:
+        vt = (bias if bias is not None else gate).dtype
+        vec_f32 = _vector_type(vt)
+        if bias is not None:
+            bp = _vector("bias", bias, 1, rows, vt, dev)[0]
+        if gate is not None:
+            gp, gb = _vector("gate", gate, B, N, vt, dev)
+    if out is None:
+        out = _allocate(stream, torch.empty, shape, dtype=bf16, device=x.device)
+    op, ob, orow = _token_rows("out", out, shape, bf16, dev)
+    rc = lib.flux_linear_fp8(xp, xb, xr, xsp, xsb, xsr, xsk, wp, wr, wsp, wsr, wsk, B, S, K, N,
+                             code, bp, gp, gb, vec_f32, rp, rb, rr, op, ob, orow,
+                             _status_pointer(lib, status, dev), handle)
+    if rc != 0:
+        raise FluxError("flux_linear_fp8", rc, lib)
+    return out
+
+
+def _status_pointer(lib, status, dev):
+    """A caller's status word (int32 [1]), or the device's own."""
+    import torch
+
+    if status is None:
+        return _own_words.get(dev) or _own_status(lib, dev)
+    if status.dtype != torch.int32 or status.numel() < 1 or status.get_device() != dev:
+        raise ValueError(f"status must hold one int32 on cuda:{dev}")
+    return status.data_ptr()
 
 
 _own_words = {}  # address of the library's own status word, by device

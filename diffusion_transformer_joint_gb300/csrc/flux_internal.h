@@ -181,6 +181,58 @@ cudaError_t launch_linear_split(const LinearProblem &q, const SplitPlan &plan,
                                 const LinearEpilogue &epi, int act, int *status,
                                 cudaStream_t stream);
 
+// x [B, S, K] (bf16, or fp32 with x_f32) to e4m3 q and fp32 scales per `rows`
+// rows (1, or 128 with B = 1) and 128 channels. K a multiple of 16; strides in
+// elements: x_*, q_* as the token tensors of LinearFp8Problem, s_bs, s_rs, s_ks
+// between the scales of batch elements, rows (of blocks) and groups.
+struct QuantizeFp8 {
+  const void *x;
+  void *q;
+  float *scale;
+  int64_t x_bs, x_rs, q_bs, q_rs, s_bs, s_rs, s_ks;
+  int64_t B, S;
+  int K, rows, x_f32;
+};
+cudaError_t launch_quantize_fp8(const QuantizeFp8 &q, cudaStream_t stream);
+
+// out = residual + gate * act(x W^T + bias) over tokens [B, S]: x and W e4m3
+// with fp32 scales per 128 channels of a token (xs) and per 128 x 128 block of W
+// (ws). Strides in elements: x_* and w_rs multiples of 16, r_* and o_* of 8, the
+// scales' any that are not negative (_ks from one group of channels to the next).
+struct LinearFp8Problem {
+  const void *x, *w, *residual;
+  void *out;
+  const float *xs, *ws;
+  int64_t x_bs, x_rs, w_rs, r_bs, r_rs, o_bs, o_rs, xs_bs, xs_rs, xs_ks, ws_rs, ws_ks;
+  int64_t B, S, N;
+  int K;
+};
+
+// How a problem runs: split (units of one CTA over Q tokens, the channels in C
+// parts) or else pairs of CTAs (tiles of tn accumulator columns), each with an
+// estimate of its time in ns.
+struct Fp8SplitPlan {
+  int Q, C, stages;
+  bool early;
+  double ns;
+};
+struct Fp8PairPlan {
+  int tn;
+  double ns;
+};
+struct Fp8Plan {
+  bool use_split;
+  Fp8SplitPlan split;
+  Fp8PairPlan pair;
+};
+Fp8SplitPlan plan_fp8_split(const LinearFp8Problem &q, int act, int sms);
+Fp8PairPlan plan_fp8_pair(const LinearFp8Problem &q, int act, int sms);
+Fp8Plan plan_linear_fp8(const LinearFp8Problem &q, int act, int sms);
+cudaError_t launch_fp8_split(const LinearFp8Problem &q, const Fp8SplitPlan &plan,
+                             const LinearEpilogue &epi, int act, int *status, cudaStream_t stream);
+cudaError_t launch_fp8_pair(const LinearFp8Problem &q, const Fp8PairPlan &plan,
+                            const LinearEpilogue &epi, int act, int *status, cudaStream_t stream);
+
 // x_out = x + gate * y, h = norm(x_out) * (1 + scale) + shift over tokens
 // [B, S] of `dim` channels. x and x_out are bf16, or fp32 with stream_f32; y
 // and h bf16; gate, scale and shift bf16, or fp32 with vec_f32. y NULL: no

@@ -92,6 +92,20 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 
+// After an abort the even CTA of a pair counts no further copies, but the odd
+// one may still have issued some into stages that were free; they complete on
+// the even CTA's barriers in a phase that nobody ends, and the odd CTA, whose
+// accumulators are committed all the same, would not stay for them. The even
+// CTA's producer stays a millisecond (a copy lands within some microseconds, and
+// none is issued later: the MMAs that free stages stop with the abort), and with
+// it the cluster, which no CTA leaves before all have arrived at its last barrier.
+constexpr long long kHoldCycles = 2000000;
+__device__ __forceinline__ void hold_after_abort() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < kHoldCycles) {
+  }
+}
+
 // What the plans' estimates (ns) share: an SM takes in about 112 bytes per ns;
 // a stage's 64 channels are four MMAs of N / 2 cycles, about N ns. Fitted, like
 // the constants beside them, to the times of every form at 103 problems of 1 to

@@ -102,20 +102,6 @@ struct SplitMaps {
   CUtensorMap x, x2, w, w2;
 };
 
-// After an abort the even CTA of a pair counts no further copies, but the odd
-// one may still have issued some into stages that were free; they complete on
-// the even CTA's barriers in a phase that nobody ends, and the odd CTA, whose
-// accumulators are committed all the same, would not stay for them. The even
-// CTA's producer stays a millisecond (a copy lands within some microseconds, and
-// none is issued later: the MMAs that free stages stop with the abort), and with
-// it the cluster, which no CTA leaves before all have arrived at its last barrier.
-constexpr long long kHoldCycles = 2000000;
-__device__ __forceinline__ void hold_after_abort() {
-  const long long t0 = clock64();
-  while (clock64() - t0 < kHoldCycles) {
-  }
-}
-
 __device__ __forceinline__ void add4(float4 &v, float4 a) {
   v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
 }

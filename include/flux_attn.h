@@ -481,6 +481,62 @@ int flux_modulated_norm(const void *x, int64_t x_bs, int64_t x_rs, int stream_f3
                         void *stream);
 
 /*
+ * Products in 8-bit floating point. Operands are e4m3 (one byte: sign, four
+ * exponent bits of bias 7, three of mantissa; largest value 448), each with an
+ * fp32 scale per group that its values are multiplied with: a group is 128
+ * channels of a token (activations), or 128 rows x 128 channels (weights); the
+ * last groups of a row or column may be shorter. Scales may lie in any order:
+ * strides, in elements, between batch elements (_bs), tokens or row blocks
+ * (_rs) and groups of channels (_ks); where the library reads them, 0 spreads
+ * one scale over an axis. e4m3 rows have strides that are multiples of 16.
+ */
+
+/*
+ * flux_quantize_fp8: rows or a weight to e4m3 with its scales,
+ *   t = max(max |x| over the group, 2^-100),  scale = t / 448,
+ *   q = e4m3(x * (448 / t)),
+ * each operation in fp32, to nearest even. A group that holds an infinity or a
+ * NaN has a scale that is not finite, and stands for NaN throughout.
+ *
+ *   x          device, bf16 [B, S, K], or fp32 with x_f32 = 1.
+ *   K          a multiple of 16, at most 2^22.  1 <= B * S <= 2^30.
+ *   rows       of a group: 1 (scale [B, S, ceil(K / 128)]), or 128 with B = 1
+ *              and S at most 2^22 (scale [ceil(S / 128), ceil(K / 128)]).
+ *   q          e4m3 [B, S, K].
+ *   scale      fp32, 4-byte aligned; no two of its elements share their place.
+ *              Tokens beside one another (s_rs = 1) are written, and read by
+ *              flux_linear_fp8, in whole memory lines.
+ * Returns FLUX_OK when the kernel was enqueued, else a negative status.
+ */
+int flux_quantize_fp8(const void *x, int64_t x_bs, int64_t x_rs, int x_f32, int B, int64_t S, int K,
+                      int rows, void *q, int64_t q_bs, int64_t q_rs, float *scale, int64_t s_bs,
+                      int64_t s_rs, int64_t s_ks, void *stream);
+
+/*
+ * flux_linear_fp8: flux_linear over such operands,
+ *   y[t, n] = sum_g x_scale[t, g] w_scale[n / 128, g] sum_{k in g} x[t, k] w[n, k] + bias[n],
+ *   out = residual + gate * act(y), rounded once to bf16 (nearest even).
+ * A group's products are summed by the tensor core in fp32, the groups by fp32
+ * fused multiply-adds.
+ *
+ *   x          device, e4m3 [B, S, K]; K a multiple of 16, at most 2^22.
+ *   x_scale    fp32 [B, S, ceil(K / 128)].
+ *   w, w_rs    device, e4m3 [N, K] with row stride w_rs; for FLUX_ACT_SWIGLU
+ *              [2 N, K], the N gate rows, then the N linear rows, N a multiple
+ *              of 128.
+ *   w_scale    fp32 [ceil(rows of w / 128), ceil(K / 128)].
+ *   B, S, N, act, bias, gate, residual, out, status  as for flux_linear.
+ * The sums are added in an order that depends on the sizes only.
+ * Returns FLUX_OK when the kernel was enqueued, else a negative status.
+ */
+int flux_linear_fp8(const void *x, int64_t x_bs, int64_t x_rs, const float *x_scale, int64_t xs_bs,
+                    int64_t xs_rs, int64_t xs_ks, const void *w, int64_t w_rs,
+                    const float *w_scale, int64_t ws_rs, int64_t ws_ks, int B, int64_t S, int K,
+                    int64_t N, int act, const void *bias, const void *gate, int64_t gate_bs,
+                    int vec_f32, const void *residual, int64_t r_bs, int64_t r_rs, void *out,
+                    int64_t o_bs, int64_t o_rs, int32_t *status, void *stream);
+
+/*
  * flux_joint_qknorm_rope_attention_extract / _cached: the two KV modes with
  * the QK RMS normalisation before RoPE (as flux_joint_qknorm_rope_attention:
  * text tokens, the first S_txt, with the text weights; every other token,
