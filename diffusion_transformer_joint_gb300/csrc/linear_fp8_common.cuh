@@ -1,5 +1,4 @@
-// What the two kernels behind flux_linear_fp8 share: tensor maps over 8-bit rows
-// and the ring through which a group's scales reach the warps that add its sums.
+// What the two kernels behind flux_linear_fp8 share: tensor maps over 8-bit rows.
 #pragma once
 
 #include "linear_common.cuh"

@@ -15,15 +15,15 @@
 // What that costs: a group's 128 x tn sums per SM are read from TMEM (128 KB at
 // tn = 256) and take as many FMAs, in the 512 cycles that the group's MMAs last.
 // So one warpgroup adds a half: thread = TMEM lane = token row, its up to 128
-// running sums in registers (setmaxnreg gives the two warpgroups 216 each). A
-// half of a group is read while the other half's MMAs run, and has three halves'
-// time (768 cycles) from its last MMA until its columns are wanted again; with
-// one accumulator of 256 columns, twice, it had 512, less than the hand-off
-// between the two took.
+// running sums in registers (setmaxnreg). A half of a group is read while the
+// other half's MMAs run, and has three halves' time (768 cycles) from its last MMA
+// until its columns are wanted again. Its hand-back to the even CTA's issuer is an
+// arrival without a release, which waits for the thread's stores: with one, a
+// group took 1.3 us instead of 0.7.
 //
-// The scales come through a ring of their own, filled by warp 3 of each CTA:
-// xs of the CTA's 128 tokens and ws of the tile's 32-column pieces; it keeps four
-// groups' loads in flight (a load takes longer than a group's MMAs).
+// Warp 3 of each CTA brings the scales, four groups at a time, to a ring in shared
+// memory: every other way took the sums' warps longer, which set the pace (a
+// barrier's wait per group, some 100 cycles; copies of their own, 130).
 //
 // SwiGLU: a half's columns are gate features and the linear features of the same
 // outputs, so that a thread has both factors of what it writes.
@@ -34,8 +34,10 @@
 // groups. A residual's boxes are fetched while the tile's groups are added: three
 // boxes a warp and five stages of ring with one, else two and six.
 //
-// 12 warps per CTA: warp 0 TMA producer, warp 1 MMA issuer (even CTA), warp 2
-// TMEM allocation, warp 3 scales, warps 4-7 and 8-11 the two halves.
+// 12 warps per CTA: warp 0 TMA producer, warps 1 and 2 MMA issuers of a half each
+// (even CTA; one warp for both took longer to issue a group's MMAs, between waits
+// of some 100 cycles, than they run), warp 2 TMEM allocation, warps 4-7 and 8-11
+// the sums of the two halves.
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -55,15 +57,14 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int kMaxBoxes = 3;             // boxes per epilogue warp
 constexpr uint32_t kBoxBytes = 32 * 64;  // 32 rows x 32 features
-constexpr int kScaleSlots = 4;
-constexpr int kScaleBatch = 4;
-constexpr uint32_t kScaleBytes = (kRows + 8) * 4;  // xs of the rows, ws of 2 x 4 pieces
-constexpr int kBarFull = 0;                        // (even CTA) both CTAs' copies landed
-constexpr int kBarEmpty = kMaxStages;              // the pair's MMAs read the stage
-constexpr int kBarAccFull = 2 * kMaxStages;        // + 2 * buffer + half
-constexpr int kBarAccEmpty = kBarAccFull + 4;      // (even CTA) both CTAs read it
+constexpr int kScaleSlots = 2, kScaleBatch = 4;  // slots, of so many groups
+constexpr uint32_t kScaleBytes = kRows * 4 + 16;  // a group: the rows', two of W's per half
+constexpr int kBarFull = 0;                    // (even CTA) both CTAs' copies landed
+constexpr int kBarEmpty = kMaxStages;          // the pair's MMAs read the stage
+constexpr int kBarAccFull = 2 * kMaxStages;    // + 2 * buffer + half
+constexpr int kBarAccEmpty = kBarAccFull + 4;  // (even CTA) both CTAs read it
 constexpr int kBarDrain = kBarAccEmpty + 4;
-constexpr int kBarScFull = kBarDrain + 1;
+constexpr int kBarScFull = kBarDrain + 2;
 constexpr int kBarScEmpty = kBarScFull + kScaleSlots;
 constexpr int kBarRes = kBarScEmpty + kScaleSlots;  // residual box landed, per warp and box
 constexpr int kBarVecReady = kBarRes + kEpiWarps * kMaxBoxes;
@@ -71,21 +72,25 @@ constexpr int kBarVecFree = kBarVecReady + 1;
 constexpr int kNumBars = kBarVecFree + 1;
 // shared memory from here on is behind the ring and the boxes
 constexpr uint32_t kOffScale = 0;
-constexpr uint32_t kOffVec = kScaleSlots * kScaleBytes;  // a tile's bias, gate
+constexpr uint32_t kOffVec = kScaleSlots * kScaleBatch * kScaleBytes;  // a tile's bias, gate
 constexpr uint32_t kOffBar = kOffVec + 2 * kMaxTn * 4;
 constexpr uint32_t kOffTmemSlot = kOffBar + 8 * kNumBars;
 constexpr uint32_t kOffAbort = kOffTmemSlot + 8;
 constexpr uint32_t kTailBytes = kOffAbort + 8;
 constexpr uint32_t kSmemMax = 232448;
 constexpr uint16_t kPairMask = 0x3;
-// registers: 384 threads x 168 at launch
-constexpr uint32_t kRegsSum = 216, kRegsRest = 72;
-static_assert(2 * kRegsSum + kRegsRest == 3 * 168, "warpgroups' shares of the registers");
+// Registers: 384 threads x 168 at launch. More for the sums is not always better
+// (12800 x 18432 -> 6144: 1.10 ms with 200, 1.18 with 216, 1.27 with 192; 4056 x
+// 4096 -> SwiGLU 12288: 368 us with 216, 403 with 200).
+template <bool kGlu>
+constexpr uint32_t kSumRegs = kGlu ? 216 : 200;
+template <bool kGlu>
+constexpr uint32_t kRestRegs = 3 * 168 - 2 * kSumRegs<kGlu>;
 
 struct PairShape {
   int64_t S, N, xs_bs, xs_rs, xs_ks, ws_rs, ws_ks;
   const float *xs, *ws;
-  int tn, stages, boxes, nk;
+  int stages, boxes, nk;
   int n_sb, n_rb, n_ft, n_tiles;  // row blocks per batch element, in all; feature tiles
   uint32_t off_box, off_tail;
 };
@@ -119,14 +124,15 @@ __device__ __forceinline__ void add8(float (&v)[8], const float *p) {
 }
 
 // acc += s * (32 sums as loaded from TMEM)
-__device__ __forceinline__ void add_scaled(uint64_t *acc, const uint32_t (&v)[32], float s) {
+__device__ __forceinline__ void add_scaled(uint64_t *acc, const uint64_t (&v)[16], float s) {
   const uint64_t s2 = f2_pack(s, s);
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    acc[i] = f2_fma(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2, acc[i]);
+  for (int i = 0; i < 16; ++i) asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i]) : "l"(v[i]), "l"(s2));
 }
 
-template <int kAct>
+// kPieces: 32-column pieces of a half, tn = 64 kPieces. (As a launch parameter it
+// cost a third more time: running sums were moved between registers.)
+template <int kAct, int kPieces>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_fp8_pair_kernel(const __grid_constant__ PairMaps maps, const PairShape p,
                            const LinearEpilogue epi, const int has_res, int *__restrict__ status) {
@@ -135,7 +141,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_addr(base);
   const uint32_t tail = sbase + p.off_tail;
   auto bar = [&](int i) { return tail + kOffBar + 8u * static_cast<uint32_t>(i); };
-  auto sc_slot = [&](int i) { return tail + kOffScale + kScaleBytes * static_cast<uint32_t>(i); };
+  auto scales_at = [&](int i) {  // group i of the ring's slots
+    return tail + kOffScale + kScaleBytes * static_cast<uint32_t>(i);
+  };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + p.off_tail + kOffTmemSlot);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(base + p.off_tail + kOffAbort);
   const int tid = static_cast<int>(threadIdx.x);
@@ -144,22 +152,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t crank = cluster_ctarank();  // 0: issues the MMAs
   const int cid = static_cast<int>(cluster_id_x());
   const int ncl = static_cast<int>(cluster_count_x());
-  const int hw = p.tn / 2;                   // columns of a half
-  const int feats = kGlu ? hw : p.tn;        // output features per tile
-  const int hfeats = feats / 2;              // of a half
-  const uint32_t half_bytes = static_cast<uint32_t>(hw / 2) * kGroupK;  // W rows of this CTA
-  const uint32_t stage_bytes = kABytes + 2 * half_bytes;
+  constexpr int tn = 64 * kPieces;           // accumulator columns
+  constexpr int hw = tn / 2;                 // columns of a half
+  constexpr int feats = kGlu ? hw : tn;      // output features per tile
+  constexpr int hfeats = feats / 2;          // of a half
+  constexpr uint32_t half_bytes = static_cast<uint32_t>(hw / 2) * kGroupK;  // W rows of this CTA
+  constexpr uint32_t stage_bytes = kABytes + 2 * half_bytes;
 
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(bar(kBarFull + s), 1);
-      mbar_init(bar(kBarEmpty + s), 1);
+      mbar_init(bar(kBarEmpty + s), 2);  // both halves' MMAs
     }
     for (int b = 0; b < 4; ++b) {
       mbar_init(bar(kBarAccFull + b), 1);
       mbar_init(bar(kBarAccEmpty + b), kEpiWarps);  // a half's four warps of both CTAs
     }
-    mbar_init(bar(kBarDrain), 1);
+    for (int h = 0; h < 2; ++h) mbar_init(bar(kBarDrain + h), 1);
     for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(bar(kBarScFull + i), 1);
       mbar_init(bar(kBarScEmpty + i), kEpiWarps);
@@ -182,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch_dependents();
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs<kGlu>));
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------- TMA producer
       tma_prefetch_desc(&maps.x);
@@ -204,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s0 = (rb - b * p.n_sb) * (2 * kRows) + static_cast<int>(crank) * kRows;
         const int w0 = w_row(ft, 0), w1 = w_row(ft, 1);
         for (int g = 0; g < p.nk; ++g) {
-          if (!(ok = mbar_wait_cluster(bar(kBarEmpty + s), (turn & 1u) ^ 1u, abort_flag))) break;
+          if (!(ok = mbar_wait(bar(kBarEmpty + s), (turn & 1u) ^ 1u, abort_flag))) break;
           const uint32_t dst = sbase + s * stage_bytes;
           // both CTAs' copies complete on the even CTA's stage barrier
           if (crank == 0) mbar_arrive_expect_tx(bar(kBarFull + s), 2 * stage_bytes);
@@ -231,93 +240,87 @@ __global__ void __launch_bounds__(kThreads, 1)
           hold_after_abort();
         }
       }
-    } else if (warp == 1 && crank == 0) {
-      // ---------------------------------------------- MMA issuer (even CTA)
+    } else if ((warp == 1 || warp == 2) && crank == 0) {
+      // ------------------------------ MMA issuers (even CTA), one for each half
+      const uint32_t h = static_cast<uint32_t>(warp - 1);
       const uint32_t idesc = idesc_e4m3_f32(2 * kRows, hw);
       int s = 0;
       uint32_t turn = 0, n = 0;  // n: groups so far
       bool ok = true;
       grid_dep_wait();  // the budget of the first stage's wait begins with its copy
       for (int t = cid; ok && t < p.n_tiles; t += ncl) {
-        for (int g = 0; ok && g < p.nk; ++g, ++n) {
-          const uint32_t buf = n & 1u, par = ((n >> 1) & 1u) ^ 1u;
-          if (!(ok = __all_sync(0xffffffffu,
-                                mbar_wait_cluster(bar(kBarFull + s), turn & 1u, abort_flag))))
+        for (int g = 0; g < p.nk; ++g, ++n) {
+          const uint32_t a = 2 * (n & 1u) + h, par = ((n >> 1) & 1u) ^ 1u;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarFull + s), turn & 1u, abort_flag) &&
+                                                 mbar_wait(bar(kBarAccEmpty + a), par, abort_flag))))
             break;
-          const uint64_t da = sdesc_sw128(sbase + s * stage_bytes, 16, 1024);
+          tc_fence_after_sync();
+          const uint32_t st = sbase + s * stage_bytes;
+          const uint64_t da = sdesc_sw128(st, 16, 1024);
+          const uint64_t db = sdesc_sw128(st + kABytes + h * half_bytes, 16, 1024);
 #pragma unroll
-          for (uint32_t h = 0; h < 2; ++h) {
-            const uint32_t db_at = sbase + s * stage_bytes + kABytes + h * half_bytes;
-            const uint64_t db = sdesc_sw128(db_at, 16, 1024);
-            const uint32_t a = 2 * buf + h;
-            if (!(ok = __all_sync(0xffffffffu,
-                                  mbar_wait_cluster(bar(kBarAccEmpty + a), par, abort_flag))))
-              break;
-            tc_fence_after_sync();
-#pragma unroll
-            for (int kk = 0; kk < kGroupK / 32; ++kk)
-              mma_f8_pair_elect(tmem + a * kMaxHalf, desc_advance(da, kk * 32),
-                                desc_advance(db, kk * 32), idesc, kk != 0 ? 1u : 0u);
-            mma_commit_pair_elect(bar(kBarAccFull + a), kPairMask);
-          }
-          if (!ok) break;
-          mma_commit_pair_elect(bar(kBarEmpty + s), kPairMask);  // both CTAs may refill
+          for (int kk = 0; kk < kGroupK / 32; ++kk)
+            mma_f8_pair_elect(tmem + a * kMaxHalf, desc_advance(da, kk * 32),
+                              desc_advance(db, kk * 32), idesc, kk != 0 ? 1u : 0u);
+          mma_commit_pair_elect(bar(kBarAccFull + a), kPairMask);
+          mma_commit_pair_elect(bar(kBarEmpty + s), kPairMask);  // (and the other half's)
           if (++s == p.stages) s = 0, ++turn;
         }
       }
       // every MMA issued above has finished before TMEM is released
-      mma_commit_pair_elect(bar(kBarDrain), 0x1);
-      if (!mbar_settled(bar(kBarDrain), 0, clock64() + kWaitBudgetCycles)) *abort_flag = 1;
+      mma_commit_pair_elect(bar(kBarDrain + static_cast<int>(h)), 0x1);
+      if (!mbar_settled(bar(kBarDrain + static_cast<int>(h)), 0, clock64() + kWaitBudgetCycles))
+        *abort_flag = 1;
       __syncwarp();
     } else if (warp == 3) {
       // ------------------------------------------------------------- scales
-      // xs of rows lane, lane + 32, ...; lane 4 h + k: ws of piece k of half h
+      // Rows lane, lane + 32, ...; lane 2 h + i: W's block i of half h, the first
+      // and the last one of its features (SwiGLU: of its gate and linear ones).
       int slot = 0;
       uint32_t use = 0;
       bool ok = true;
-      const int64_t last_block = ((kGlu ? 2 * p.N : p.N) + 127) / 128 - 1;
+      const int N = static_cast<int>(p.N);
       grid_dep_wait();
       for (int t = cid; ok && t < p.n_tiles; t += ncl) {
         int ft, rb;
         tile_at(p, t, ft, rb);
         const int b = rb / p.n_sb;
         const int s0 = (rb - b * p.n_sb) * (2 * kRows) + static_cast<int>(crank) * kRows;
+        const int rows = static_cast<int>(p.S) - s0 - lane;  // from this lane's first one on
         const float *xs = p.xs + b * p.xs_bs + (s0 + lane) * p.xs_rs;
-        const int k = lane & 3;
-        int64_t f = static_cast<int64_t>(ft) * feats + ((lane >> 2) & 1) * hfeats;
-        f += kGlu ? (k >> 1) * p.N + 32 * (k & 1) : 32 * k;
-        const int64_t block = f / 128 < last_block ? f / 128 : last_block;
-        const float *ws = p.ws + block * p.ws_rs;
-        for (int g0 = 0; ok && g0 < p.nk; g0 += kScaleBatch) {
+        int f = ft * feats + ((lane >> 1) & 1) * hfeats;
+        if (lane & 1) f += kGlu ? N : hw - 1;
+        const int last = (kGlu ? 2 * N : N) - 1;
+        const float *ws = p.ws + ((f < last ? f : last) / 128) * p.ws_rs;
+        for (int g0 = 0; g0 < p.nk; g0 += kScaleBatch) {
           float x[kScaleBatch][4], w[kScaleBatch];
 #pragma unroll
           for (int i = 0; i < kScaleBatch; ++i) {
-            const int g = g0 + i < p.nk ? g0 + i : p.nk - 1;
-            w[i] = lane < 8 ? ws[g * p.ws_ks] : 0.f;
+            w[i] = lane < 4 ? *ws : 0.f;
+            const float *at = xs;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              x[i][j] = s0 + lane + 32 * j < p.S ? xs[32 * j * p.xs_rs + g * p.xs_ks] : 0.f;
+            for (int j = 0; j < 4; ++j, at += 32 * p.xs_rs) x[i][j] = 32 * j < rows ? *at : 0.f;
+            if (g0 + i + 1 < p.nk) xs += p.xs_ks, ws += p.ws_ks;  // (past the end: the last again)
           }
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarScEmpty + slot), (use & 1u) ^ 1u,
+                                                       abort_flag))))
+            break;
 #pragma unroll
           for (int i = 0; i < kScaleBatch; ++i) {
-            if (g0 + i >= p.nk) break;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarScEmpty + slot), (use & 1u) ^ 1u,
-                                                         abort_flag))))
-              break;
-            const uint32_t at = sc_slot(slot) + static_cast<uint32_t>(lane) * 4;
+            const uint32_t at = scales_at(slot * kScaleBatch + i) + static_cast<uint32_t>(lane) * 4;
 #pragma unroll
             for (int j = 0; j < 4; ++j) st_shared_b32(at + j * 128, __float_as_uint(x[i][j]));
-            if (lane < 8) st_shared_b32(at + kRows * 4, __float_as_uint(w[i]));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarScFull + slot));
-            if (++slot == kScaleSlots) slot = 0, ++use;
+            if (lane < 4) st_shared_b32(at + kRows * 4, __float_as_uint(w[i]));
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarScFull + slot));
+          if (++slot == kScaleSlots) slot = 0, ++use;
         }
       }
     }
   } else {
     // ------------------------------------------------------ sums and epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs<kGlu>));
     const int wq = warp & 3;            // TMEM lane quadrant
     const int h = (warp - 4) >> 2;      // half of the columns
     const int et = tid - 128;
@@ -329,14 +332,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *vec_bias = reinterpret_cast<float *>(base + p.off_tail + kOffVec);
     float *vec_gate = vec_bias + kMaxTn;
     const bool vecs = epi.bias != nullptr || epi.gate != nullptr;
-    // piece k: 32 columns of the half from its first one on (SwiGLU: two of the
-    // gate features, then two of the linear features)
-    const int n_piece = kGlu ? hw / 64 : hw / 32;  // (SwiGLU: of each kind)
     int load_slot = 0, store_slot = 0;  // this warp's boxes: residual asked for, staged
     uint32_t res_par = 0;               // bit i: parity of box i's next residual
     int loads_ahead = 0;
-    int slot = 0;
-    uint32_t sc_use = 0, n = 0;
+    int slot = 0;         // of the scales
+    uint32_t sc_use = 0;
+    bool ready = false;   // the next accumulator was complete when last looked at
+    uint32_t n = 0;
     int lt = 0;
     bool ok = true;
     grid_dep_wait();
@@ -346,18 +348,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b = rb / p.n_sb;
       const int sc = (rb - b * p.n_sb) * (2 * kRows) + static_cast<int>(crank) * kRows;
       const int s0 = sc + wq * 32;
-      const int64_t f0 = static_cast<int64_t>(ft) * feats;  // of the tile
-      const int64_t fh = f0 + h * hfeats;                   // of the half
-      const int64_t left = p.N - fh;
+      const int N = static_cast<int>(p.N);  // (at most 2^28, and tiles end below 2^29)
+      const int f0 = ft * feats;            // of the tile
+      const int fh = f0 + h * hfeats;       // of the half
+      const int left = N - fh;
       // boxes of this tile that hold anything to write
       const int n_box = s0 >= p.S || left <= 0
                             ? 0
-                            : static_cast<int>(left < hfeats ? (left + 31) / 32 : hfeats / 32);
+                            : left < hfeats ? (left + 31) / 32 : hfeats / 32;
+      // pieces whose columns have W's first block of the half
+      const int in_first = kGlu ? kPieces / 2 : ((fh / 128 + 1) * 128 - fh) / 32;
       auto load_residual = [&](int c) {  // a box whose store has read it
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(bar_res + load_slot), kBoxBytes);
           tma_load_3d(boxes + load_slot * kBoxBytes, &maps.res, bar(bar_res + load_slot),
-                      static_cast<int>(fh) + c * 32, s0, b);
+                      fh + c * 32, s0, b);
         }
         if (++load_slot == p.boxes) load_slot = 0;
         ++loads_ahead;
@@ -383,12 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         mbar_wait(bar(kBarVecFree),
                                                   static_cast<uint32_t>(lt - 1) & 1u, abort_flag))))
           break;
-        if (epi.bias != nullptr && et < p.tn) {
-          const int64_t f = f0 + (kGlu && et >= feats ? et - feats : et);
-          if (f < p.N)
-            vec_bias[et] = load_vec1(epi.bias, kGlu && et >= feats ? p.N + f : f, epi.vec_f32);
+        if (epi.bias != nullptr && et < tn) {
+          const int f = f0 + (kGlu && et >= feats ? et - feats : et);
+          if (f < N)
+            vec_bias[et] = load_vec1(epi.bias, kGlu && et >= feats ? N + f : f, epi.vec_f32);
         }
-        if (epi.gate != nullptr && !gate_rowwise && et < feats && f0 + et < p.N)
+        if (epi.gate != nullptr && !gate_rowwise && et < feats && f0 + et < N)
           vec_gate[et] = load_vec1(epi.gate, gate_row * epi.gate_bs + f0 + et, epi.vec_f32);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarVecReady));
@@ -401,83 +406,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         gate_row = r / epi.gate_rows;
       }
 
-      uint64_t acc[kMaxHalf / 2];  // pairs of sums, 16 to a piece
+      uint64_t acc[16 * kPieces];  // pairs of sums
 #pragma unroll
-      for (int i = 0; i < kMaxHalf / 2; ++i) acc[i] = 0;
+      for (int i = 0; i < 16 * kPieces; ++i) acc[i] = 0;
 #pragma unroll 1
       for (int g = 0; g < p.nk; ++g, ++n) {
         const uint32_t a = 2 * (n & 1u) + static_cast<uint32_t>(h);
-        if (!(ok = __all_sync(0xffffffffu,
+        const int in_slot = g % kScaleBatch;
+        if (in_slot == 0 &&
+            !(ok = __all_sync(0xffffffffu,
                               mbar_wait(bar(kBarScFull + slot), sc_use & 1u, abort_flag))))
           break;
-        const float xs = ld_shared_f32(sc_slot(slot) + static_cast<uint32_t>(wq * 32 + lane) * 4);
-        const float4 ws = ld_shared_f4(sc_slot(slot) + (kRows + 4 * h) * 4);
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar(kBarAccFull + a), (n >> 1) & 1u,
-                                                             abort_flag))))
+        const uint32_t scales = scales_at(slot * kScaleBatch + in_slot);
+        const float xs = ld_shared_f32(scales + static_cast<uint32_t>(wq * 32 + lane) * 4);
+        const uint2 ws = ld_shared_v2(scales + kRows * 4 + 8 * h);
+        if (!__all_sync(0xffffffffu, ready) &&
+            !(ok = __all_sync(0xffffffffu,
+                              mbar_wait(bar(kBarAccFull + a), (n >> 1) & 1u, abort_flag))))
           break;
+        const float sa = xs * __uint_as_float(ws.x), sb = xs * __uint_as_float(ws.y);
         tc_fence_after_sync();
         const uint32_t from = tmem + a * kMaxHalf + lane_off;
-        uint32_t u[32], v[32];
-        if constexpr (kGlu) {
-          const uint32_t lin = from + static_cast<uint32_t>(hw / 2);
-          tmem_ld32(from, u);
-          tmem_ld_wait(u);
-          tmem_ld32(lin, v);
-          add_scaled(acc, u, xs * ws.x);
-          tmem_ld_wait(v);
-          if (n_piece > 1) {
-            tmem_ld32(from + 32, u);
-            add_scaled(acc + 32, v, xs * ws.z);
-            tmem_ld_wait(u);
-            tmem_ld32(lin + 32, v);
-            add_scaled(acc + 16, u, xs * ws.y);
-            tmem_ld_wait(v);
+        // a piece at a time through the same registers: the FMAs are the bound (290
+        // cycles a group for the two warps of a scheduler), the loads take 6 more
+        // each; two pieces' registers in turn took half as long again
+        uint64_t v[16];
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+          tmem_ld32_pairs(from + k * 32, v);
+          if (k == kPieces - 1) {
+            // this warp's TMEM reads are complete: the columns may be reused
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + 8u * a);
+            // a look at the next group's, whose answer comes while these are added
+            ready = mbar_try_wait(bar(kBarAccFull + static_cast<int>(a ^ 2u)), ((n + 1) >> 1) & 1u);
           }
-        } else {
-          tmem_ld32(from, u);
-          tmem_ld_wait(u);
-          if (n_piece > 1) {
-            tmem_ld32(from + 32, v);
-            add_scaled(acc, u, xs * ws.x);
-            tmem_ld_wait(v);
-            if (n_piece > 2) {
-              tmem_ld32(from + 64, u);
-              add_scaled(acc + 16, v, xs * ws.y);
-              tmem_ld_wait(u);
-              if (n_piece > 3) {
-                tmem_ld32(from + 96, v);
-                add_scaled(acc + 32, u, xs * ws.z);
-                tmem_ld_wait(v);
-              }
-            }
-          }
+          add_scaled(acc + k * 16, v, k < in_first ? sa : sb);
         }
-        // this warp's TMEM reads are complete: the columns may be reused
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster(acc_empty0 + 8u * a);
-          mbar_arrive(bar(kBarScEmpty + slot));
+        if (in_slot == kScaleBatch - 1 || g == p.nk - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarScEmpty + slot));
+          if (++slot == kScaleSlots) slot = 0, ++sc_use;
         }
-        // the piece read last
-        if constexpr (kGlu) {
-          if (n_piece > 1)
-            add_scaled(acc + 48, v, xs * ws.w);
-          else
-            add_scaled(acc + 32, v, xs * ws.z);
-        } else {
-          if (n_piece == 1) add_scaled(acc, u, xs * ws.x);
-          if (n_piece == 2) add_scaled(acc + 16, v, xs * ws.y);
-          if (n_piece == 3) add_scaled(acc + 32, u, xs * ws.z);
-          if (n_piece == 4) add_scaled(acc + 48, v, xs * ws.w);
-        }
-        if (++slot == kScaleSlots) slot = 0, ++sc_use;
       }
       if (!ok) break;
 
       // 32 features at a time: the rows' values into a box, which one copy stores
 #pragma unroll
-      for (int c = 0; c < kMaxHalf / 32 / (kGlu ? 2 : 1); ++c) {
+      for (int c = 0; c < hfeats / 32; ++c) {
         if (c >= n_box) break;
         const uint32_t box = boxes + store_slot * kBoxBytes;
         if (has_res) {
@@ -490,50 +467,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) bulk_wait_read_1();
           __syncwarp();
         }
+        const uint32_t row = box + lane * 64, turn = static_cast<uint32_t>(lane >> 1) & 3u;
+        const int quads = left - c * 32 < 32 ? (left - c * 32) / 8 : 4;
+        uint4 r[4];
+        if (has_res) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) r[q] = ld_shared_v4(row + ((q ^ turn) << 4));
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int64_t f = fh + c * 32 + q * 8;
-          const uint32_t at = box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
-          if (f < p.N) {
-            const int v0 = h * hfeats + c * 32 + q * 8;  // in the tile's vectors
-            float y[8];
+          if (q >= quads) break;
+          const int v0 = h * hfeats + c * 32 + q * 8;  // in the tile's vectors
+          float y[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f2_unpack(acc[c * 16 + q * 4 + i], y[2 * i], y[2 * i + 1]);
-            if (epi.bias != nullptr) add8(y, vec_bias + v0);
-            if constexpr (kGlu) {
-              float w[8];
+          for (int i = 0; i < 4; ++i) f2_unpack(acc[c * 16 + q * 4 + i], y[2 * i], y[2 * i + 1]);
+          if (epi.bias != nullptr) add8(y, vec_bias + v0);
+          if constexpr (kGlu) {
+            float w[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                f2_unpack(acc[32 + c * 16 + q * 4 + i], w[2 * i], w[2 * i + 1]);
-              if (epi.bias != nullptr) add8(w, vec_bias + feats + v0);
+            for (int i = 0; i < 4; ++i)
+              f2_unpack(acc[8 * kPieces + c * 16 + q * 4 + i], w[2 * i], w[2 * i + 1]);
+            if (epi.bias != nullptr) add8(w, vec_bias + feats + v0);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = activate<FLUX_ACT_SILU>(y[i]) * w[i];
-            } else {
+            for (int i = 0; i < 8; ++i) y[i] = activate<FLUX_ACT_SILU>(y[i]) * w[i];
+          } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = activate<kAct>(y[i]);
-            }
-            if (epi.gate != nullptr) {
-              float w[8];
-              if (gate_rowwise)
-                load_vec8(epi.gate, gate_row * epi.gate_bs + f, epi.vec_f32, w);
-              else
-                read8(w, vec_gate + v0);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] *= w[i];
-            }
-            if (has_res) {
-              float w[8];
-              unpack8(ld_shared_v4(at), w);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] += w[i];
-            }
-            st_shared_v4(at, pack8(y));
+            for (int i = 0; i < 8; ++i) y[i] = activate<kAct>(y[i]);
           }
+          if (epi.gate != nullptr) {
+            float w[8];
+            if (gate_rowwise)
+              load_vec8(epi.gate, gate_row * epi.gate_bs + fh + c * 32 + q * 8, epi.vec_f32, w);
+            else
+              read8(w, vec_gate + v0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] *= w[i];
+          }
+          if (has_res) {
+            float w[8];
+            unpack8(r[q], w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] += w[i];
+          }
+          r[q] = pack8(y);
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < quads) st_shared_v4(row + ((q ^ turn) << 4), r[q]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(&maps.out, box, static_cast<int>(fh) + c * 32, s0, b);
+          tma_store_3d(&maps.out, box, fh + c * 32, s0, b);
           bulk_commit();
         }
         if (++store_slot == p.boxes) store_slot = 0;
@@ -570,8 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && *abort_flag) atomicExch(status, FLUX_ERR_DEVICE_TIMEOUT);
 }
 
-template <int kAct>
-cudaError_t launch(const LinearFp8Problem &q, int tn, const LinearEpilogue &epi, int *status,
+template <int kAct, int kPieces>
+cudaError_t launch(const LinearFp8Problem &q, const LinearEpilogue &epi, int *status,
                    cudaStream_t stream) {
   static std::once_flag attr_once[64];
   static cudaError_t attr_err[64];
@@ -580,7 +564,8 @@ cudaError_t launch(const LinearFp8Problem &q, int tn, const LinearEpilogue &epi,
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kernel = linear_fp8_pair_kernel<kAct>;
+  auto kernel = linear_fp8_pair_kernel<kAct, kPieces>;
+  constexpr int tn = 64 * kPieces;
   std::call_once(attr_once[dev], [&] {
     attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSmemMax));
@@ -591,7 +576,6 @@ cudaError_t launch(const LinearFp8Problem &q, int tn, const LinearEpilogue &epi,
   p.S = q.S, p.N = q.N;
   p.xs_bs = q.xs_bs, p.xs_rs = q.xs_rs, p.xs_ks = q.xs_ks, p.ws_rs = q.ws_rs, p.ws_ks = q.ws_ks;
   p.xs = q.xs, p.ws = q.ws;
-  p.tn = tn;
   p.boxes = q.residual != nullptr ? kMaxBoxes : 2;
   const uint32_t stage = kABytes + static_cast<uint32_t>(tn / 2) * kGroupK;
   const uint32_t box_bytes = static_cast<uint32_t>(kEpiWarps * p.boxes) * kBoxBytes;
@@ -646,6 +630,18 @@ cudaError_t launch(const LinearFp8Problem &q, int tn, const LinearEpilogue &epi,
   cfg.numAttrs = 2;
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
   return cudaLaunchKernelEx(&cfg, kernel, maps, p, epi, q.residual != nullptr ? 1 : 0, status);
+}
+
+template <int kAct>
+cudaError_t launch(const LinearFp8Problem &q, int tn, const LinearEpilogue &epi, int *status,
+                   cudaStream_t stream) {
+  if (tn == 256) return launch<kAct, 4>(q, epi, status, stream);
+  if (tn == 128) return launch<kAct, 2>(q, epi, status, stream);
+  if constexpr (kAct != FLUX_ACT_SWIGLU) {
+    if (tn == 192) return launch<kAct, 3>(q, epi, status, stream);
+    if (tn == 64) return launch<kAct, 1>(q, epi, status, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
