@@ -32,8 +32,8 @@ EXPORTS = ("flux_rope_tables", "flux_rope_tables_packed", "flux_joint_rope_atten
            "flux_joint_rope_attention_cached_workspace", "flux_joint_rope_attention_cached",
            "flux_joint_qknorm_rope_attention_extract", "flux_joint_qknorm_rope_attention_cached",
            "flux_qkv_mlp_proj", "flux_linear", "flux_modulated_norm", "flux_quantize_fp8",
-           "flux_linear_fp8", "flux_query_status", "flux_status_word", "flux_take_status",
-           "flux_status_string")
+           "flux_linear_fp8", "flux_cross_attention", "flux_query_status", "flux_status_word",
+           "flux_take_status", "flux_status_string")
 
 
 class FluxError(RuntimeError):
@@ -135,6 +135,9 @@ def load(path: str | None = None):
                                             I32, I64, I32, I64, I32, V, V, I64, I32, V, I64, I64,
                                             V, I64, I64, V, V]
             lib.flux_linear_fp8.restype = I32
+            lib.flux_cross_attention.argtypes = [V, I64, I64, V, I64, I64, V, I64, I64, V, V, I64,
+                                                 I32, I64, I64, I32, I32, I32, F, V, I64, I64, V, V]
+            lib.flux_cross_attention.restype = I32
             lib.flux_query_status.argtypes = [V, V]
             lib.flux_query_status.restype = I32
             lib.flux_status_word.argtypes = [V]
@@ -958,6 +961,77 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, act=None, gate=None, residual=
                              _status_pointer(lib, status, dev), handle)
     if rc != 0:
         raise FluxError("flux_linear_fp8", rc, lib)
+    return out
+
+
+def _head_rows(name, t, shape, dev):
+    """(address, batch stride, token stride) of bf16 heads [B, S, H, D], a token's
+    heads adjacent; raises for anything else."""
+    import torch
+
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    bs, rs, hs, cs = t.stride()
+    if cs != 1 or (hs != shape[3] and shape[2] > 1):
+        raise ValueError(f"{name} must have a token's heads adjacent, got strides {t.stride()}")
+    return t.data_ptr(), bs, rs
+
+
+def cross_attention(q, k, v, lengths=None, mask=None, scale=None, out=None, status=None,
+                    stream=None):
+    """Attention to another sequence: softmax(scale q k^T) v over the keys that take part.
+
+    q: bf16 CUDA [B, Sq, H, D], D 64 or 128; k, v bf16 [B, Sk, Hk, D], Hk a
+    divisor of H (query heads in groups of H / Hk share a key head); strides
+    between tokens and batch elements (two halves of one product's output).
+    lengths: int32 [B], keys from there on take no part; mask: bool or uint8 [B,
+    Sk], nor do keys where it is 0 (their k and v may hold anything). A row that
+    no key is left for is zero. scale: 1 / sqrt(D) unless given. ``out`` bf16 of
+    q's shape; ``status`` as for linear. Returns out.
+    """
+    import torch
+
+    lib = _lib or load()
+    dev, handle = _stream_of(q, stream)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q and k must be [B, S, H, D], got {tuple(q.shape)}, {tuple(k.shape)}")
+    B, Sq, H, D = shape = q.shape
+    Sk, Hk = k.shape[1], k.shape[2]
+    if max(B, H, Hk) > 0x7FFFFFFF:
+        raise ValueError(f"batch and heads must be below 2^31, got {B}, {H}, {Hk}")
+    qp, qb, qr = _head_rows("q", q, shape, dev)
+    kp, kb, kr = _head_rows("k", k, (B, Sk, Hk, D), dev)
+    vp, vb, vr = _head_rows("v", v, (B, Sk, Hk, D), dev)
+    lp = mp = None
+    mb = 0
+    if lengths is not None:
+        if lengths.shape != (B,) or lengths.dtype != torch.int32 or lengths.get_device() != dev \
+                or not lengths.is_contiguous():
+            raise ValueError(f"lengths must be contiguous int32 [{B}] on cuda:{dev}, got "
+                             f"{lengths.dtype} {tuple(lengths.shape)} on {lengths.device}")
+        lp = lengths.data_ptr()
+    if mask is not None:
+        if mask.shape != (B, Sk) or mask.dtype not in (torch.bool, torch.uint8) \
+                or mask.get_device() != dev or (mask.stride(1) != 1 and Sk > 1):
+            raise ValueError(f"mask must be bool or uint8 [{B}, {Sk}] on cuda:{dev} with its keys "
+                             f"adjacent, got {mask.dtype} {tuple(mask.shape)} on {mask.device}")
+        mp, mb = mask.data_ptr(), mask.stride(0) if B > 1 else 0
+    if scale is None:
+        scale = 0.0
+    elif not 0.0 < scale < 3e38:
+        raise ValueError(f"scale must be finite and positive, got {scale}")
+    if out is None:
+        out = _allocate(stream, torch.empty, shape, dtype=torch.bfloat16, device=q.device)
+    op, ob, orow = _head_rows("out", out, shape, dev)
+    rc = lib.flux_cross_attention(qp, qb, qr, kp, kb, kr, vp, vb, vr, lp, mp, mb, B, Sq, Sk, H, Hk,
+                                  D, float(scale), op, ob, orow, _status_pointer(lib, status, dev),
+                                  handle)
+    if rc != 0:
+        raise FluxError("flux_cross_attention", rc, lib)
     return out
 
 

@@ -233,6 +233,31 @@ cudaError_t launch_fp8_split(const LinearFp8Problem &q, const Fp8SplitPlan &plan
 cudaError_t launch_fp8_pair(const LinearFp8Problem &q, const Fp8PairPlan &plan,
                             const LinearEpilogue &epi, int act, int *status, cudaStream_t stream);
 
+// out = softmax(scale q k^T) v, bf16 q and out [B, Sq, H, D], k and v [B, Sk, Hk,
+// D], D 64 or 128, Hk a divisor of H and H / Hk at most 128. Strides in elements,
+// heads adjacent. lengths (int32 [B]) and mask (bytes [B, Sk] at stride mask_bs),
+// each nullable, say which keys take part.
+struct CrossAttention {
+  const void *q, *k, *v;
+  void *out;
+  const int32_t *lengths;
+  const uint8_t *mask;
+  int64_t q_bs, q_rs, k_bs, k_rs, v_bs, v_rs, o_bs, o_rs, mask_bs;
+  int64_t B, Sq, Sk;
+  int H, Hk, D;
+  float scale;
+};
+// The form that runs: narrow, with the keys in `parts` parts, or else wide; and
+// an estimate of its time in ns.
+struct CrossPlan {
+  bool narrow;
+  int parts;
+  double ns;
+};
+CrossPlan plan_cross(const CrossAttention &a, int sms);
+cudaError_t launch_cross_attention(const CrossAttention &a, const CrossPlan &plan, int *status,
+                                   cudaStream_t stream);
+
 // x_out = x + gate * y, h = norm(x_out) * (1 + scale) + shift over tokens
 // [B, S] of `dim` channels. x and x_out are bf16, or fp32 with stream_f32; y
 // and h bf16; gate, scale and shift bf16, or fp32 with vec_f32. y NULL: no

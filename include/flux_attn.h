@@ -537,6 +537,37 @@ int flux_linear_fp8(const void *x, int64_t x_bs, int64_t x_rs, const float *x_sc
                     int64_t o_bs, int64_t o_rs, int32_t *status, void *stream);
 
 /*
+ * flux_cross_attention: attention to another sequence (an encoder's states),
+ *   out[b, i, h] = sum_j softmax_j(scale q[b, i, h] . k[b, j, h / G]) v[b, j, h / G],
+ * G = H / Hk, over the keys j that take part: j below lengths[b], and mask[b, j]
+ * not 0. What k and v hold for the others is not looked at (it may be NaN). A
+ * row that no key is left for is 0. Sums and the softmax are fp32, the weights
+ * are rounded to bf16 for the product with v, and each output once to bf16.
+ *
+ *   q          device, bf16 [B, Sq, H, D], D 64 or 128: a token's heads are
+ *              adjacent; strides between tokens (_rs) and batch elements (_bs) as
+ *              for flux_linear's rows.
+ *   k, v       bf16 [B, Sk, Hk, D] with strides of their own (two halves of one
+ *              product's rows, say); Hk divides H, H / Hk at most 128.
+ *   lengths    device int32 [B], or NULL (Sk each); taken as 0 below 0 and as Sk
+ *              above Sk.
+ *   mask       device bytes [B, Sk] at batch stride mask_bs (0: one for all), or
+ *              NULL (all 1). Any alignment.
+ *   B, Sq, Sk  1 <= B * Sq, B * Sk <= 2^30; at most 2^24 blocks of 128 Hk / H
+ *              queries (rounded down) per key head of all batch elements.
+ *   scale      finite, > 0; 0 stands for 1 / sqrt(D).
+ *   out        bf16 [B, Sq, H, D].
+ *   status     as for flux_linear.
+ * The sums are added in an order that depends on the sizes only.
+ * Returns FLUX_OK when the kernel was enqueued, else a negative status.
+ */
+int flux_cross_attention(const void *q, int64_t q_bs, int64_t q_rs, const void *k, int64_t k_bs,
+                         int64_t k_rs, const void *v, int64_t v_bs, int64_t v_rs,
+                         const int32_t *lengths, const uint8_t *mask, int64_t mask_bs, int B,
+                         int64_t Sq, int64_t Sk, int H, int Hk, int D, float scale, void *out,
+                         int64_t o_bs, int64_t o_rs, int32_t *status, void *stream);
+
+/*
  * flux_joint_qknorm_rope_attention_extract / _cached: the two KV modes with
  * the QK RMS normalisation before RoPE (as flux_joint_qknorm_rope_attention:
  * text tokens, the first S_txt, with the text weights; every other token,
