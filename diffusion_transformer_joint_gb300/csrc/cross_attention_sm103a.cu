@@ -28,7 +28,7 @@
 //           no workspace, no second launch, the same order in every run.
 //
 // 16 warps: warp 0 TMA producer of Q and K, warp 1 MMA issuer, warp 2 TMEM
-// allocation and masks (a tile's key bits, V rows that take no part zeroed),
+// allocation, V rows that take no part zeroed (masks),
 // warp 3 TMA producer of V; warps 4-7 and 8-11 the softmax of stream 0 and 1
 // (thread = TMEM lane = row), warps 12-15 the epilogue, so that a stream's softmax
 // goes on with the next item while its O is read.
@@ -57,9 +57,9 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLowest = -3.0e38f;        // a maximum no key has been counted in
 constexpr uint32_t kBlockBytes = 16384;    // 128 rows x 64 channels, one swizzle block
 constexpr uint32_t kBoxBytes = 32 * 64;    // epilogue: 32 rows x 32 channels
-constexpr int kBoxes = 2;                  // per epilogue warp
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxUnits = 8;
+constexpr int kAll = 0, kLengths = 1, kMask = 2;
+constexpr int kMaxParts = 16;  // of the keys: CTAs of a cluster
 // registers: 512 threads x 128 at launch
 constexpr uint32_t kRegsSoftmax = 168, kRegsCopyMma = 72, kRegsEpilogue = 104;
 static_assert(2 * kRegsSoftmax + kRegsCopyMma + kRegsEpilogue == 4 * 128, "register shares");
@@ -72,9 +72,8 @@ struct Layout {
   static constexpr uint32_t kOffK = kQTiles * kTileBytes;
   static constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
   static constexpr uint32_t kOffBox = kOffV + kStages * kTileBytes;
-  static constexpr uint32_t kOffRow = kOffBox + (kNarrow ? 0 : 4 * kBoxes * kBoxBytes);
-  static constexpr uint32_t kOffBits = kOffRow + 2 * 2 * kTile * 4;  // m and l of a stream's rows
-  static constexpr uint32_t kOffBar = kOffBits + kStages * 16;
+  static constexpr uint32_t kOffRow = kOffBox + (kNarrow ? 0 : 4 * (kD / 32) * kBoxBytes);
+  static constexpr uint32_t kOffBar = kOffRow + 2 * 2 * kTile * 4;  // (m and l of a stream's rows)
   // barriers
   static constexpr int kQFull = 0, kQFree = 2, kKFull = 4, kKEmpty = kKFull + kStages;
   static constexpr int kVRaw = kKEmpty + kStages, kVFull = kVRaw + kStages;
@@ -162,7 +161,8 @@ __device__ __forceinline__ void tma_store_5d(const void *tmap, uint32_t src, int
       : "memory");
 }
 
-template <int kD, bool kNarrow, bool kMasked>
+// kKeys: all keys take part, or those below a length, or those of a mask too.
+template <int kD, bool kNarrow, int kKeys>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_attention_kernel(const __grid_constant__ Maps maps, const Shape p, int *status) {
   using L = Layout<kD, kNarrow>;
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     it.b = bh / p.Hk;
     it.s0 = rb * p.n_s * L::kQTiles;
     it.keys = p.Sk;
-    if constexpr (kMasked) {
+    if constexpr (kKeys != kAll) {
       if (p.lengths != nullptr) {
         if (it.b != len_b) {
           len_b = it.b;
@@ -240,6 +240,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     it.lo = kNarrow ? static_cast<int>(static_cast<int64_t>(n) * part / p.parts) : 0;
     it.n = (kNarrow ? static_cast<int>(static_cast<int64_t>(n) * (part + 1) / p.parts) : n) - it.lo;
     return it;
+  };
+
+  // Which keys of tile j take part, 32 a word, all of a warp's lanes together.
+  auto key_bits = [&](const Item &it, int j, uint32_t (&bits)[4]) {
+    const int valid = it.keys - (it.lo + j) * kTile;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int n = valid - 32 * w;
+      bits[w] = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    }
+    if constexpr (kKeys == kMask) {
+      const uint8_t *row = p.mask + it.b * p.mask_bs + (it.lo + j) * kTile + lane;
+      uint8_t in[4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) in[w] = (bits[w] >> lane) & 1u ? row[32 * w] : 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) bits[w] = __ballot_sync(0xffffffffu, in[w] != 0);
+    }
+  };
+  // A tile of V some of whose rows may have to be zeroed lands on V-raw and is
+  // passed on to V-full by the mask warp, other ones land on V-full.
+  auto v_raw = [&](const Item &it, int j) {
+    return kKeys == kMask || (kKeys == kLengths && it.keys - (it.lo + j) * kTile < kTile);
   };
 
   if (warp < 4) {
@@ -297,69 +320,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&maps.v);
       int s = 0;
       uint32_t turn = 0;
+      uint32_t raw_par = 0, last_raw = 0;  // bit s: V-raw's next parity; the last copy's barrier
       bool ok = true;
-      const int landed = kMasked ? L::kVRaw : L::kVFull;
       for (int i = first; ok && i < p.n_items; i += step) {
         const Item it = item_at(i);
         for (int j = 0; j < it.n; ++j) {
           if (!(ok = mbar_wait(bar(L::kVEmpty + s), (turn & 1u) ^ 1u, abort_flag))) break;
           const uint32_t dst = sbase + L::kOffV + static_cast<uint32_t>(s) * L::kTileBytes;
-          mbar_arrive_expect_tx(bar(landed + s), L::kTileBytes);
+          const bool raw = v_raw(it, j);
+          const uint32_t landed = bar((raw ? L::kVRaw : L::kVFull) + s);
+          last_raw = (last_raw & ~(1u << s)) | (raw ? 1u << s : 0u);
+          if (raw) raw_par ^= 1u << s;
+          mbar_arrive_expect_tx(landed, L::kTileBytes);
           for (int c = 0; c < kD / 64; ++c)
-            tma_load_4d(dst + c * kBlockBytes, &maps.v, bar(landed + s), c * 64, it.h,
-                        (it.lo + j) * kTile, it.b);
+            tma_load_4d(dst + c * kBlockBytes, &maps.v, landed, c * 64, it.h, (it.lo + j) * kTile,
+                        it.b);
           if (++s == kStages) s = 0, ++turn;
         }
       }
       if (!ok) {
         const long long until = clock64() + kWaitBudgetCycles;
         for (int i = 0; i < kStages; ++i) {
-          if (i < s)
-            (void)mbar_settled(bar(landed + i), turn & 1u, until);
-          else if (turn > 0)
-            (void)mbar_settled(bar(landed + i), (turn - 1) & 1u, until);
+          if (i >= s && turn == 0) continue;
+          if ((last_raw >> i) & 1u)
+            (void)mbar_settled(bar(L::kVRaw + i), ((raw_par >> i) & 1u) ^ 1u, until);
+          else
+            (void)mbar_settled(bar(L::kVFull + i), (i < s ? turn : turn - 1) & 1u, until);
         }
       }
-    } else if (kMasked && warp == 2) {
+    } else if (kKeys != kAll && warp == 2) {
       // ------------------------------------------------------------- masks
       int s = 0;
-      uint32_t turn = 0;
+      uint32_t raw_par = 0;
       bool ok = true;
       for (int i = first; ok && i < p.n_items; i += step) {
         const Item it = item_at(i);
-        for (int j = 0; j < it.n; ++j) {
-          // the tile's key bits: 32 keys a word, one per lane
-          const int key0 = (it.lo + j) * kTile;
+        for (int j = 0; j < it.n; ++j, s = s + 1 == kStages ? 0 : s + 1) {
+          if (!v_raw(it, j)) continue;
           uint32_t bits[4];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int key = key0 + 32 * w + lane;
-            bool in = key < it.keys;
-            if (in && p.mask != nullptr) in = p.mask[it.b * p.mask_bs + key] != 0;
-            bits[w] = __ballot_sync(0xffffffffu, in);
-          }
-          if (!(ok = wait_warp(bar(L::kVRaw + s), turn & 1u, abort_flag))) break;
-          if (lane == 0)
-            st_shared_v4(sbase + L::kOffBits + static_cast<uint32_t>(s) * 16,
-                         make_uint4(bits[0], bits[1], bits[2], bits[3]));
-          // the tile's V rows that take no part: eight lanes a row of a block
+          key_bits(it, j, bits);
+          if (!(ok = wait_warp(bar(L::kVRaw + s), (raw_par >> s) & 1u, abort_flag))) break;
+          raw_par ^= 1u << s;
+          // the V rows that take no part, one per lane, its chunks in an order that
+          // keeps eight lanes in different banks
           const uint32_t tile = sbase + L::kOffV + static_cast<uint32_t>(s) * L::kTileBytes;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             if (bits[w] == 0xffffffffu) continue;
-#pragma unroll 1
-            for (int r = 0; r < 32; r += 4) {
-              const int row = r + (lane >> 3);
-              if ((bits[w] >> row) & 1u) continue;
-              for (int c = 0; c < kD / 64; ++c)
-                st_shared_v4(tile + c * kBlockBytes + static_cast<uint32_t>(32 * w + row) * 128 +
-                                 (lane & 7) * 16,
-                             make_uint4(0u, 0u, 0u, 0u));
-            }
+            if ((bits[w] >> lane) & 1u) continue;
+#pragma unroll
+            for (int c = 0; c < kD / 8; ++c)
+              st_shared_v4(tile + (c >> 3) * kBlockBytes + static_cast<uint32_t>(32 * w + lane) * 128 +
+                               static_cast<uint32_t>((c ^ lane) & 7) * 16,
+                           make_uint4(0u, 0u, 0u, 0u));
           }
-          fence_proxy_async_smem();
+          if ((bits[0] & bits[1] & bits[2] & bits[3]) != 0xffffffffu) fence_proxy_async_smem();
           warp_arrive(bar(L::kVFull + s), lane);
-          if (++s == kStages) s = 0, ++turn;
         }
       }
     } else if (warp == 1) {
@@ -426,9 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) mma_commit_elect(bar(L::kKEmpty));
           kr.next();
         }
+        // the tile after, found while the products run
+        auto after = [&](At a) { return ++a.j < a.n ? a : from(a.i + step, a.k + 1); };
+        At nx = at.i < p.n_items ? after(at) : at;
         while (ok && at.i < p.n_items) {
-          At nx = at;
-          if (++nx.j == nx.n) nx = from(at.i + step, at.k + 1);
           const bool more = nx.i < p.n_items, last = at.j == at.n - 1;
           if (!(ok = wait_warp(bar(L::kVFull + vr.s), vr.turn & 1u, abort_flag))) break;
 #pragma unroll
@@ -454,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           vr.next();
           if (more) kr.next();
           at = nx;
+          if (more) nx = after(nx);
           ++g;
         }
       } else {
@@ -508,19 +526,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale_log2 = p.scale_log2;
     bool ok = true;
     uint32_t g = 0, k = 0;  // the stream's tiles and items so far
-    int vs = 0;             // ring position of V (masks): of the item's first tile
-    uint32_t vturn = 0;
     for (int i = first; ok && i < p.n_items; i += step) {
       const Item it = item_at(i);
       float m_run = kLowest, l_run = 0.f;
       bool fresh = true;
+      // a warp without rows of the tensor takes part in the hand-offs only (its P
+      // is whatever was there, for rows that nobody reads)
+      const int s_tile = it.s0 + (kNarrow ? 0 : t * p.n_s);
+      const bool idle = wq * 32 >= (p.Sq - s_tile < p.n_s ? p.Sq - s_tile : p.n_s) * p.G;
       for (int j = 0; j < it.n; ++j) {
-        const int s = vs;
-        const uint32_t par = vturn & 1u;
-        if (++vs == kStages) vs = 0, ++vturn;
         if (kNarrow && (j & 1) != t) continue;
+        uint32_t bits[4];  // (a mask's, while the scores are on their way)
+        if constexpr (kKeys == kMask) key_bits(it, j, bits);
         if (!(ok = wait_warp(bar(L::kSFull + t), g & 1u, abort_flag))) break;
         tc_fence_after_sync();
+        if (idle) {
+          ++g;
+          tc_fence_before_sync();
+          warp_arrive(bar(L::kPFull + t), lane);
+          continue;
+        }
         uint32_t sr[kTile];
         float mr[4];
 #pragma unroll
@@ -528,20 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32_max(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]), mr[c]);
         tmem_ld_wait();
         float mx = fmax3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
-        uint32_t bits[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        if constexpr (kMasked) {
-          if (!(ok = wait_warp(bar(L::kVFull + s), par, abort_flag))) break;
-          const uint4 w = ld_shared_v4(sbase + L::kOffBits + static_cast<uint32_t>(s) * 16);
-          bits[0] = w.x, bits[1] = w.y, bits[2] = w.z, bits[3] = w.w;
-        } else {
-          const int valid = it.keys - (it.lo + j) * kTile;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int n = valid - 32 * w;
-            bits[w] = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-          }
-        }
-        if ((bits[0] & bits[1] & bits[2] & bits[3]) != 0xffffffffu) {
+        const bool all = kKeys == kMask
+                             ? (bits[0] & bits[1] & bits[2] & bits[3]) == 0xffffffffu
+                             : it.keys - (it.lo + j) * kTile >= kTile;
+        if (!all) {
+          if constexpr (kKeys != kMask) key_bits(it, j, bits);
           mx = -INFINITY;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -631,7 +647,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qh = row - qs * p.G;
     bool ok = true;
     uint32_t k = 0, k_o[2] = {0, 0};             // items with keys, with keys of a stream
-    int box = 0;
     for (int i = first; ok && i < p.n_items; i += step) {
       const Item it = item_at(i);
       if constexpr (!kNarrow) {
@@ -647,50 +662,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = wait_warp(bar(L::kODone + t), k & 1u, abort_flag))) break;
             tc_fence_after_sync();
           }
+          // the row's values to registers as bf16, and O is free for the next item
           const uint32_t tO = tmem + 256 + t * 128 + lane_off;
-          uint16_t *to = p.out + it.b * p.o_bs + static_cast<int64_t>(s) * p.o_rs +
-                         static_cast<int64_t>(it.h * p.G + qh) * kD;
-          const int box_s = s_tile + wq * 32 / p.G;  // first query of the warp's box
-#pragma unroll 1
+          uint4 w[kD / 8];
+#pragma unroll
           for (int c = 0; c < kD / 32; ++c) {
             uint32_t o[32];
             if (it.n > 0) {
               tmem_ld32(tO + c * 32, o);
               tmem_ld_wait();
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0;
             }
-            uint4 w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              auto v = [&](int e) { return __uint_as_float(o[8 * q + e]) * inv_l; };
-              w[q] = make_uint4(pack_bf16x2(v(0), v(1)), pack_bf16x2(v(2), v(3)),
-                                pack_bf16x2(v(4), v(5)), pack_bf16x2(v(6), v(7)));
-            }
-            if (p.boxed) {
-              const uint32_t stage =
-                  sbase + L::kOffBox + static_cast<uint32_t>(((warp - 12) * kBoxes + box)) * kBoxBytes;
-              if (lane == 0) bulk_wait_read_1();  // the box's last copy has read it
-              __syncwarp();
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                st_shared_v4(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), w[q]);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (box_s < p.Sq) tma_store_5d(&maps.out, stage, c * 32, 0, it.h, box_s, it.b);
-                bulk_commit();
-              }
-              box ^= 1;
-            } else if (row_ok) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) st_global_v4(to + c * 32 + q * 8, w[q]);
+              auto v = [&](int e) {
+                return it.n > 0 ? __uint_as_float(o[8 * q + e]) * inv_l : 0.f;
+              };
+              w[c * 4 + q] = make_uint4(pack_bf16x2(v(0), v(1)), pack_bf16x2(v(2), v(3)),
+                                        pack_bf16x2(v(4), v(5)), pack_bf16x2(v(6), v(7)));
             }
           }
           if (it.n > 0) {
             tc_fence_before_sync();
             warp_arrive(bar(L::kOFree + t), lane);
+          }
+          if (p.boxed) {
+            const uint32_t boxes = sbase + L::kOffBox +
+                                   static_cast<uint32_t>((warp - 12) * (kD / 32)) * kBoxBytes;
+            const int box_s = s_tile + wq * 32 / p.G;  // first query of the warp's boxes
+            if (lane == 0) bulk_wait_read_all();  // the copies before have read the boxes
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < kD / 8; ++q)
+              st_shared_v4(boxes + (q >> 2) * kBoxBytes + lane * 64 +
+                               (((q & 3) ^ ((lane >> 1) & 3)) << 4),
+                           w[q]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && box_s < p.Sq) {
+              for (int c = 0; c < kD / 32; ++c)
+                tma_store_5d(&maps.out, boxes + c * kBoxBytes, c * 32, 0, it.h, box_s, it.b);
+              bulk_commit();
+            }
+          } else if (row_ok) {
+            uint16_t *to = p.out + it.b * p.o_bs + static_cast<int64_t>(s) * p.o_rs +
+                           static_cast<int64_t>(it.h * p.G + qh) * kD;
+#pragma unroll
+            for (int q = 0; q < kD / 8; ++q) st_global_v4(to + q * 8, w[q]);
           }
         }
         if (!ok) break;
@@ -779,28 +796,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hi = static_cast<int>(static_cast<int64_t>(units) * (part + 1) / p.parts);
     for (int u = lo + tid; u < hi; u += kThreads) {
       const int row = u / (kD / 4), c = u - row * (kD / 4);
-      float m[kMaxUnits], l[kMaxUnits], top = kLowest;
-      float4 o[kMaxUnits];
-#pragma unroll
-      for (int r = 0; r < kMaxUnits; ++r) {
-        if (r < p.parts) {
-          m[r] = ld_cluster_f32(mapa_shared(row_at(0, 0, row), r));
-          l[r] = ld_cluster_f32(mapa_shared(row_at(0, 1, row), r));
-          o[r] = ld_cluster_f4(mapa_shared(
-              sbase + L::kOffK + static_cast<uint32_t>(row) * L::kPitch + c * 16, r));
-          top = fmaxf(top, m[r]);
-        }
-      }
+      float top = kLowest;
+#pragma unroll 4
+      for (int r = 0; r < p.parts; ++r)
+        top = fmaxf(top, ld_cluster_f32(mapa_shared(row_at(0, 0, row), r)));
       float sum = 0.f;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int r = 0; r < kMaxUnits; ++r) {
-        if (r < p.parts) {
-          const float w = ex2_approx(m[r] - top);
-          sum = fmaf(w, l[r], sum);
-          v.x = fmaf(w, o[r].x, v.x), v.y = fmaf(w, o[r].y, v.y);
-          v.z = fmaf(w, o[r].z, v.z), v.w = fmaf(w, o[r].w, v.w);
-        }
+#pragma unroll 4
+      for (int r = 0; r < p.parts; ++r) {
+        const float w = ex2_approx(ld_cluster_f32(mapa_shared(row_at(0, 0, row), r)) - top);
+        const float4 o = ld_cluster_f4(mapa_shared(
+            sbase + L::kOffK + static_cast<uint32_t>(row) * L::kPitch + c * 16, r));
+        sum = fmaf(w, ld_cluster_f32(mapa_shared(row_at(0, 1, row), r)), sum);
+        v.x = fmaf(w, o.x, v.x), v.y = fmaf(w, o.y, v.y);
+        v.z = fmaf(w, o.z, v.z), v.w = fmaf(w, o.w, v.w);
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int qs = row / p.G, qh = row - qs * p.G;
@@ -851,7 +860,7 @@ bool make_map(CUtensorMap *map, const void *x, int D, int G, int Hk, int64_t S, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kD, bool kNarrow, bool kMasked>
+template <int kD, bool kNarrow, int kKeys>
 cudaError_t launch(const CrossAttention &a, const CrossPlan &plan, int sms, int *status,
                    cudaStream_t stream) {
   using L = Layout<kD, kNarrow>;
@@ -861,10 +870,12 @@ cudaError_t launch(const CrossAttention &a, const CrossPlan &plan, int sms, int 
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kernel = cross_attention_kernel<kD, kNarrow, kMasked>;
+  auto kernel = cross_attention_kernel<kD, kNarrow, kKeys>;
   std::call_once(attr_once[dev], [&] {
     attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(L::kSmemBytes));
+    if (kNarrow && attr_err[dev] == cudaSuccess)  // clusters of more than eight
+      attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   });
   if (attr_err[dev] != cudaSuccess) return attr_err[dev];
   Shape p;
@@ -910,8 +921,17 @@ cudaError_t launch(const CrossAttention &a, const CrossPlan &plan, int sms, int 
   return cudaLaunchKernelEx(&cfg, kernel, maps, p, status);
 }
 
+template <int kD, bool kNarrow>
+cudaError_t launch(const CrossAttention &a, const CrossPlan &plan, int sms, int *status,
+                   cudaStream_t stream) {
+  if (a.mask != nullptr) return launch<kD, kNarrow, kMask>(a, plan, sms, status, stream);
+  if (a.lengths != nullptr) return launch<kD, kNarrow, kLengths>(a, plan, sms, status, stream);
+  return launch<kD, kNarrow, kAll>(a, plan, sms, status, stream);
+}
+
 }  // namespace
 
+constexpr int kFill16 = 112;
 CrossPlan plan_cross(const CrossAttention &a, int sms) {
   const int64_t n_s = kTile / (a.H / a.Hk), bh = a.B * a.Hk;
   const int64_t tiles = (a.Sk + kTile - 1) / kTile;
@@ -919,10 +939,12 @@ CrossPlan plan_cross(const CrossAttention &a, int sms) {
   const int64_t narrow = bh * ((a.Sq + n_s - 1) / n_s);
   auto waves = [&](int64_t n, int64_t slots) { return static_cast<double>((n + slots - 1) / slots); };
   CrossPlan best{false, 1, 2500.0 + waves(wide, sms) * (1100.0 * tiles + 1000.0)};
-  for (int parts = 1; parts <= kMaxUnits && parts <= tiles; parts *= 2) {
-    // clusters of four and eight do not fill every SM
-    const int64_t slots = parts == 8 ? sms * 120 / 152 / 8 : parts == 4 ? sms * 144 / 152 / 4
-                                                                        : sms / parts;
+  for (int parts = 1; parts <= kMaxParts && parts <= tiles; parts *= 2) {
+    // clusters of four and more do not fill every SM
+    const int64_t slots = parts == 16 ? sms * kFill16 / 152 / 16
+                          : parts == 8 ? sms * 120 / 152 / 8
+                          : parts == 4 ? sms * 144 / 152 / 4
+                                       : sms / parts;
     const double own = std::ceil(static_cast<double>(tiles) / parts);
     const double per = 600.0 * own + 1400.0 + (parts > 1 ? 4500.0 : 0.0);
     const double ns = 2500.0 + waves(narrow, std::max<int64_t>(1, slots)) * per;
@@ -935,17 +957,11 @@ cudaError_t launch_cross_attention(const CrossAttention &a, const CrossPlan &pla
                                    cudaStream_t stream) {
   const int sms = sm_count_current_device();
   if (sms < 1) return cudaErrorInvalidDevice;
-  const bool masked = a.lengths != nullptr || a.mask != nullptr;
-  switch ((a.D == 128 ? 4 : 0) | (plan.narrow ? 2 : 0) | (masked ? 1 : 0)) {
-    case 0: return launch<64, false, false>(a, plan, sms, status, stream);
-    case 1: return launch<64, false, true>(a, plan, sms, status, stream);
-    case 2: return launch<64, true, false>(a, plan, sms, status, stream);
-    case 3: return launch<64, true, true>(a, plan, sms, status, stream);
-    case 4: return launch<128, false, false>(a, plan, sms, status, stream);
-    case 5: return launch<128, false, true>(a, plan, sms, status, stream);
-    case 6: return launch<128, true, false>(a, plan, sms, status, stream);
-    default: return launch<128, true, true>(a, plan, sms, status, stream);
-  }
+  if (a.D == 64)
+    return plan.narrow ? launch<64, true>(a, plan, sms, status, stream)
+                       : launch<64, false>(a, plan, sms, status, stream);
+  return plan.narrow ? launch<128, true>(a, plan, sms, status, stream)
+                     : launch<128, false>(a, plan, sms, status, stream);
 }
 
 }  // namespace flux
