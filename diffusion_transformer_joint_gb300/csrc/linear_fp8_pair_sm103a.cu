@@ -7,8 +7,8 @@
 //
 // Tiles: 256 token rows of one batch element x tn accumulator columns, 128
 // channels (one group, 128 bytes) per pipeline stage. The columns are two halves
-// of tn / 2, an MMA of N = tn / 2 each, which TMEM holds twice over: the MMAs of
-// a group start both halves afresh, while the groups' sums before are read. The
+// of tn / 2, an MMA of N = tn / 2 each, which TMEM holds twice over or more: the
+// MMAs of a group start both halves afresh, while the groups' sums before are read. The
 // scales do not fit the tensor core's own block scaling, whose factors are
 // powers of two.
 //
@@ -49,7 +49,6 @@ namespace {
 
 constexpr int kRows = 128;  // token rows per CTA (256 per pair)
 constexpr int kMaxTn = 256;
-constexpr int kMaxHalf = kMaxTn / 2;
 constexpr int kGroup = 9;  // row blocks of a group of tiles (the walk)
 constexpr uint32_t kABytes = kRows * kGroupK;  // 16 KB: this CTA's token rows
 constexpr int kMaxStages = 10;
@@ -61,9 +60,10 @@ constexpr int kScaleSlots = 2, kScaleBatch = 4;  // slots, of so many groups
 constexpr uint32_t kScaleBytes = kRows * 4 + 16;  // a group: the rows', two of W's per half
 constexpr int kBarFull = 0;                    // (even CTA) both CTAs' copies landed
 constexpr int kBarEmpty = kMaxStages;          // the pair's MMAs read the stage
-constexpr int kBarAccFull = 2 * kMaxStages;    // + 2 * buffer + half
-constexpr int kBarAccEmpty = kBarAccFull + 4;  // (even CTA) both CTAs read it
-constexpr int kBarDrain = kBarAccEmpty + 4;
+constexpr int kMaxBufs = 8;
+constexpr int kBarAccFull = 2 * kMaxStages;               // + 2 * buffer + half
+constexpr int kBarAccEmpty = kBarAccFull + 2 * kMaxBufs;  // (even CTA) both CTAs read it
+constexpr int kBarDrain = kBarAccEmpty + 2 * kMaxBufs;
 constexpr int kBarScFull = kBarDrain + 2;
 constexpr int kBarScEmpty = kBarScFull + kScaleSlots;
 constexpr int kBarRes = kBarScEmpty + kScaleSlots;  // residual box landed, per warp and box
@@ -79,13 +79,11 @@ constexpr uint32_t kOffAbort = kOffTmemSlot + 8;
 constexpr uint32_t kTailBytes = kOffAbort + 8;
 constexpr uint32_t kSmemMax = 232448;
 constexpr uint16_t kPairMask = 0x3;
-// Registers: 384 threads x 168 at launch. More for the sums is not always better
-// (12800 x 18432 -> 6144: 1.10 ms with 200, 1.18 with 216, 1.27 with 192; 4056 x
-// 4096 -> SwiGLU 12288: 368 us with 216, 403 with 200).
-template <bool kGlu>
-constexpr uint32_t kSumRegs = kGlu ? 216 : 200;
-template <bool kGlu>
-constexpr uint32_t kRestRegs = 3 * 168 - 2 * kSumRegs<kGlu>;
+// Registers: 384 threads x 168 at launch. (Sums in pieces of 32 columns spilled at
+// any split, and a spill inside the loop is dear: 12800 x 18432 -> 6144 took 1.09
+// to 1.27 ms.)
+constexpr uint32_t kSumRegs = 216, kRestRegs = 72;
+static_assert(2 * kSumRegs + kRestRegs == 3 * 168, "warpgroups' shares of the registers");
 
 struct PairShape {
   int64_t S, N, xs_bs, xs_rs, xs_ks, ws_rs, ws_ks;
@@ -110,24 +108,30 @@ __device__ __forceinline__ void tile_at(const PairShape &p, int t, int &ft, int 
   rb = first + rem - ft * size;
 }
 
-__device__ __forceinline__ void read8(float (&v)[8], const float *p) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0];
-  const float4 b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void add8(float (&v)[8], const float *p) {
-  float w[8];
-  read8(w, p);
+// y += v, y *= v: 32 entries in shared memory, the same for all lanes.
+template <bool kMul>
+__device__ __forceinline__ void join32(float (&y)[32], const float *v) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] += w[i];
+  for (int k = 0; k < 32; k += 16) {
+    float4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = reinterpret_cast<const float4 *>(v + k)[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[k + 4 * i + e] = kMul ? y[k + 4 * i + e] * u[e] : y[k + 4 * i + e] + u[e];
+    }
+  }
 }
 
-// acc += s * (32 sums as loaded from TMEM)
-__device__ __forceinline__ void add_scaled(uint64_t *acc, const uint64_t (&v)[16], float s) {
+// acc += s * (16 sums as loaded from TMEM)
+__device__ __forceinline__ void add_scaled(uint64_t *acc, const uint64_t (&v)[8], float s) {
   const uint64_t s2 = f2_pack(s, s);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i]) : "l"(v[i]), "l"(s2));
+  for (int i = 0; i < 8; ++i)
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i]) : "l"(v[i]), "l"(s2));
 }
 
 // kPieces: 32-column pieces of a half, tn = 64 kPieces. (As a launch parameter it
@@ -154,6 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ncl = static_cast<int>(cluster_count_x());
   constexpr int tn = 64 * kPieces;           // accumulator columns
   constexpr int hw = tn / 2;                 // columns of a half
+  // accumulators that TMEM holds: a power of two
+  constexpr uint32_t bufs = tn == 64 ? 8 : tn == 128 ? 4 : 2;
   constexpr int feats = kGlu ? hw : tn;      // output features per tile
   constexpr int hfeats = feats / 2;          // of a half
   constexpr uint32_t half_bytes = static_cast<uint32_t>(hw / 2) * kGroupK;  // W rows of this CTA
@@ -164,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarFull + s), 1);
       mbar_init(bar(kBarEmpty + s), 2);  // both halves' MMAs
     }
-    for (int b = 0; b < 4; ++b) {
+    for (uint32_t b = 0; b < 2 * bufs; ++b) {
       mbar_init(bar(kBarAccFull + b), 1);
       mbar_init(bar(kBarAccEmpty + b), kEpiWarps);  // a half's four warps of both CTAs
     }
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch_dependents();
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs<kGlu>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------- TMA producer
       tma_prefetch_desc(&maps.x);
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       grid_dep_wait();  // the budget of the first stage's wait begins with its copy
       for (int t = cid; ok && t < p.n_tiles; t += ncl) {
         for (int g = 0; g < p.nk; ++g, ++n) {
-          const uint32_t a = 2 * (n & 1u) + h, par = ((n >> 1) & 1u) ^ 1u;
+          const uint32_t a = 2 * (n % bufs) + h, par = (n / bufs & 1u) ^ 1u;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarFull + s), turn & 1u, abort_flag) &&
                                                  mbar_wait(bar(kBarAccEmpty + a), par, abort_flag))))
             break;
@@ -260,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t db = sdesc_sw128(st + kABytes + h * half_bytes, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < kGroupK / 32; ++kk)
-            mma_f8_pair_elect(tmem + a * kMaxHalf, desc_advance(da, kk * 32),
+            mma_f8_pair_elect(tmem + a * hw, desc_advance(da, kk * 32),
                               desc_advance(db, kk * 32), idesc, kk != 0 ? 1u : 0u);
           mma_commit_pair_elect(bar(kBarAccFull + a), kPairMask);
           mma_commit_pair_elect(bar(kBarEmpty + s), kPairMask);  // (and the other half's)
@@ -320,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------ sums and epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs<kGlu>));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     const int wq = warp & 3;            // TMEM lane quadrant
     const int h = (warp - 4) >> 2;      // half of the columns
     const int et = tid - 128;
@@ -356,8 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_box = s0 >= p.S || left <= 0
                             ? 0
                             : left < hfeats ? (left + 31) / 32 : hfeats / 32;
-      // pieces whose columns have W's first block of the half
-      const int in_first = kGlu ? kPieces / 2 : ((fh / 128 + 1) * 128 - fh) / 32;
+      // Pieces whose columns have W's first block of the half (128, 64 or 32
+      // columns from a multiple of their number on lie in one block).
+      const int in_first = ((fh / 128 + 1) * 128 - fh) / 32;
       auto load_residual = [&](int c) {  // a box whose store has read it
         if (lane == 0) {
           mbar_arrive_expect_tx(bar(bar_res + load_slot), kBoxBytes);
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 16 * kPieces; ++i) acc[i] = 0;
 #pragma unroll 1
       for (int g = 0; g < p.nk; ++g, ++n) {
-        const uint32_t a = 2 * (n & 1u) + static_cast<uint32_t>(h);
+        const uint32_t a = 2 * (n % bufs) + static_cast<uint32_t>(h);
         const int in_slot = g % kScaleBatch;
         if (in_slot == 0 &&
             !(ok = __all_sync(0xffffffffu,
@@ -422,27 +429,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint2 ws = ld_shared_v2(scales + kRows * 4 + 8 * h);
         if (!__all_sync(0xffffffffu, ready) &&
             !(ok = __all_sync(0xffffffffu,
-                              mbar_wait(bar(kBarAccFull + a), (n >> 1) & 1u, abort_flag))))
+                              mbar_wait(bar(kBarAccFull + a), n / bufs & 1u, abort_flag))))
           break;
         const float sa = xs * __uint_as_float(ws.x), sb = xs * __uint_as_float(ws.y);
         tc_fence_after_sync();
-        const uint32_t from = tmem + a * kMaxHalf + lane_off;
+        const uint32_t from = tmem + a * hw + lane_off;
         // a piece at a time through the same registers: the FMAs are the bound (290
         // cycles a group for the two warps of a scheduler), the loads take 6 more
         // each; two pieces' registers in turn took half as long again
-        uint64_t v[16];
+        uint64_t v[8];
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-          tmem_ld32_pairs(from + k * 32, v);
-          if (k == kPieces - 1) {
+        for (int k = 0; k < 2 * kPieces; ++k) {
+          tmem_ld16_pairs(from + k * 16, v);
+          if (k == 2 * kPieces - 1) {
             // this warp's TMEM reads are complete: the columns may be reused
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + 8u * a);
             // a look at the next group's, whose answer comes while these are added
-            ready = mbar_try_wait(bar(kBarAccFull + static_cast<int>(a ^ 2u)), ((n + 1) >> 1) & 1u);
+            ready = mbar_try_wait(
+                bar(kBarAccFull + static_cast<int>(2 * ((n + 1) % bufs)) + h), (n + 1) / bufs & 1u);
           }
-          add_scaled(acc + k * 16, v, k < in_first ? sa : sb);
+          add_scaled(acc + k * 8, v,
+                     (kGlu ? k < kPieces : kPieces != 3 || k < 2 * in_first) ? sa : sb);
         }
         if (in_slot == kScaleBatch - 1 || g == p.nk - 1) {
           __syncwarp();
@@ -467,53 +476,59 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) bulk_wait_read_1();
           __syncwarp();
         }
+        // One operand at a time for all 32 features, its loads on their way together.
+        // (Features past N: whatever lies there, never stored by the copy.)
         const uint32_t row = box + lane * 64, turn = static_cast<uint32_t>(lane >> 1) & 3u;
-        const int quads = left - c * 32 < 32 ? (left - c * 32) / 8 : 4;
-        uint4 r[4];
+        const int v0 = h * hfeats + c * 32;  // in the tile's vectors
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f2_unpack(acc[c * 16 + i], y[2 * i], y[2 * i + 1]);
+        if (epi.bias != nullptr) join32<false>(y, vec_bias + v0);
+        if constexpr (kGlu) {
+          float w[32];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            f2_unpack(acc[8 * kPieces + c * 16 + i], w[2 * i], w[2 * i + 1]);
+          if (epi.bias != nullptr) join32<false>(w, vec_bias + feats + v0);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = activate<FLUX_ACT_SILU>(y[i]) * w[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = activate<kAct>(y[i]);
+        }
+        if (epi.gate != nullptr) {
+          if (gate_rowwise) {
+            for (int q = 0; q < 4; ++q) {
+              if (c * 32 + q * 8 >= left) break;
+              float w[8];
+              load_vec8(epi.gate, gate_row * epi.gate_bs + fh + c * 32 + q * 8, epi.vec_f32, w);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i >> 3 == q) y[i] *= w[i & 7];
+            }
+          } else {
+            join32<true>(y, vec_gate + v0);
+          }
+        }
         if (has_res) {
+          uint4 r[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) r[q] = ld_shared_v4(row + ((q ^ turn) << 4));
-        }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q >= quads) break;
-          const int v0 = h * hfeats + c * 32 + q * 8;  // in the tile's vectors
-          float y[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f2_unpack(acc[c * 16 + q * 4 + i], y[2 * i], y[2 * i + 1]);
-          if (epi.bias != nullptr) add8(y, vec_bias + v0);
-          if constexpr (kGlu) {
-            float w[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              f2_unpack(acc[8 * kPieces + c * 16 + q * 4 + i], w[2 * i], w[2 * i + 1]);
-            if (epi.bias != nullptr) add8(w, vec_bias + feats + v0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = activate<FLUX_ACT_SILU>(y[i]) * w[i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = activate<kAct>(y[i]);
-          }
-          if (epi.gate != nullptr) {
-            float w[8];
-            if (gate_rowwise)
-              load_vec8(epi.gate, gate_row * epi.gate_bs + fh + c * 32 + q * 8, epi.vec_f32, w);
-            else
-              read8(w, vec_gate + v0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] *= w[i];
-          }
-          if (has_res) {
+          for (int q = 0; q < 4; ++q) {
             float w[8];
             unpack8(r[q], w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] += w[i];
+            for (int i = 0; i < 8; ++i) y[q * 8 + i] += w[i];
           }
-          r[q] = pack8(y);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (q < quads) st_shared_v4(row + ((q ^ turn) << 4), r[q]);
+          st_shared_v4(row + ((q ^ turn) << 4),
+                       make_uint4(pack_bf16x2(y[q * 8], y[q * 8 + 1]),
+                                  pack_bf16x2(y[q * 8 + 2], y[q * 8 + 3]),
+                                  pack_bf16x2(y[q * 8 + 4], y[q * 8 + 5]),
+                                  pack_bf16x2(y[q * 8 + 6], y[q * 8 + 7])));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
