@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + 8u * a);
             // a look at the next group's, whose answer comes while these are added
-            ready = mbar_try_wait(
+            ready = mbar_test_wait(
                 bar(kBarAccFull + static_cast<int>(2 * ((n + 1) % bufs)) + h), (n + 1) / bufs & 1u);
           }
           add_scaled(acc + k * 8, v,
@@ -661,20 +661,32 @@ cudaError_t launch(const LinearFp8Problem &q, int tn, const LinearEpilogue &epi,
 
 }  // namespace
 
+// The tile's width: 64, 128, 192 or 256 accumulator columns (SwiGLU: 128 or 256).
+// Its estimate in ns: what a group of channels takes, the end of a tile that the
+// next one's MMAs do not hide, and a call; fitted to 194 times at 42 problems of 32
+// to 4608 tokens.
 Fp8PairPlan plan_fp8_pair(const LinearFp8Problem &q, int act, int sms) {
+  struct Costs {
+    int tn;
+    double group, tile, call;
+  };
+  static constexpr Costs kCosts[] = {{256, 432.0, 4500.0, 400.0}, {192, 397.0, 2870.0, 1330.0},
+                                     {128, 278.0, 1900.0, 2100.0}, {64, 283.0, 220.0, 3700.0}};
   const bool glu = act == FLUX_ACT_SWIGLU;
   const int64_t n_rb = q.B * ((q.S + 2 * kRows - 1) / (2 * kRows));
   const double nk = static_cast<double>((q.K + kGroupK - 1) / kGroupK);
   const int64_t pairs = std::max(1, sms / 2);
+  const int64_t wr = glu ? 2 * q.N : q.N;
+  const double bytes = static_cast<double>(q.B * q.S + wr) * q.K +
+                       2.0 * static_cast<double>(q.B * q.S) * q.N * (q.residual != nullptr ? 2 : 1);
   Fp8PairPlan best{kMaxTn, 1e30};
-  const int step = glu ? 128 : 64;
-  for (int tn = kMaxTn; tn >= step; tn -= step) {
-    const int64_t feats = glu ? tn / 2 : tn;
+  for (const Costs &t : kCosts) {
+    if (glu && t.tn % 128 != 0) continue;
+    const int64_t feats = glu ? t.tn / 2 : t.tn;
     const int64_t tiles = n_rb * ((q.N + feats - 1) / feats);
     const double waves = static_cast<double>((tiles + pairs - 1) / pairs);
-    const double ns =
-        waves * (nk * stage_ns(kABytes + tn / 2 * kGroupK, tn) + 700.0) + 3000.0;
-    if (ns < best.ns) best = Fp8PairPlan{tn, ns};
+    const double ns = std::max(t.call + waves * (nk * t.group + t.tile), bytes / 6690.0 + 4000.0);
+    if (ns < best.ns) best = Fp8PairPlan{t.tn, ns};
   }
   return best;
 }

@@ -1,5 +1,5 @@
 // flux_linear_fp8 where whole 256-row tiles would leave SMs idle (few tokens, or
-// few features), on sm_103a (GB300): tiles of 128 rows of W against up to 64
+// few features), on sm_103a (GB300): tiles of 128 rows of W against up to 192
 // tokens, the channels split over a cluster.
 //
 //   y[t, n] = sum_g xs[t, g] ws[n / 128, g] sum_{k in g} x[t, k] w[n, k]
@@ -10,21 +10,21 @@
 // A pipeline stage is one group of 128 channels. Its four K32 MMAs start a
 // fresh accumulator; eight warps read it, multiply each token's column with
 // xs[t, g] * ws[.., g] and add it to fp32 sums in registers, while the MMAs of
-// the next groups fill the other three accumulators: the products inside a group
-// are summed by the tensor core in fp32, the groups by fp32 FMAs in the order of
-// the channels.
+// the next groups fill the other accumulators (four, or two of over 128 columns):
+// the products inside a group are summed by the tensor core in fp32, the groups
+// by fp32 FMAs in the order of the channels.
 //
 // As linear_split, the groups of a tile are split over the C CTAs of a cluster
 // (an SM takes in about 110 bytes per ns, whatever the tile computes), which send
 // each other their partial sums by bulk copies; each adds the partials of its
 // share of the tokens in the CTAs' order and writes the finished rows. No
-// workspace, no atomics, one launch. CTAs allocate TMEM for their own SM only
-// and leave room for a second one there.
+// workspace, no atomics, one launch. CTAs allocate TMEM for their own SM only; up
+// to 64 tokens two share an SM.
 //
 // 12 warps: warp 0 TMA producer, warp 1 MMA issuer, warp 2 TMEM allocation,
 // warp 3 the scales: it multiplies each token's with the tile's (for SwiGLU the
-// gate rows' and the linear rows') and hands them over through a ring of its
-// own, four groups' loads in flight together. Warps 4-11 sums: one TMEM lane (a row of W) per
+// gate rows' and the linear rows') and hands them over four groups at a time (a
+// wait costs the sums' warps some 100 cycles). Warps 4-11 sums: one TMEM lane (a row of W) per
 // thread, 16 tokens at a time, the two warps of a lane quadrant taking turns.
 // Then all of them finish. Every wait is bounded, as in linear_split.
 #include <algorithm>
@@ -38,29 +38,35 @@ namespace {
 
 constexpr int kP = 128;
 constexpr uint32_t kPBytes = kP * kGroupK;
-constexpr int kMaxQ = 64;
 constexpr int kMaxStages = 8;
 constexpr int kMaxUnits = 8;
 constexpr int kThreads = 384;
 constexpr int kSumWarps = 8;
-constexpr int kBufs = 4;  // accumulators
-constexpr int kScaleSlots = 8;
-constexpr int kScaleBatch = 4;                      // groups whose scales are loaded together
-constexpr uint32_t kScaleBytes = 2 * kMaxQ * 4;     // a slot: per token, twice for SwiGLU
-constexpr uint32_t kSmemHalf = 114688;              // two CTAs on an SM
-// CTAs take no less, whatever their plan needs: beside a CTA pair of linear_split
-// (144 KB or more) an SM has no room for another that allocates TMEM.
-constexpr uint32_t kSmemLeast = 98304;
-constexpr int kBarFull = 0, kBarEmpty = kMaxStages, kBarAccFull = 2 * kMaxStages;
-constexpr int kBarAccEmpty = kBarAccFull + kBufs, kBarScFull = kBarAccEmpty + kBufs;
-constexpr int kBarScEmpty = kBarScFull + kScaleSlots, kBarDone = kBarScEmpty + kScaleSlots;
-constexpr int kBarRecv = kBarDone + 1, kNumBars = kBarRecv + 1;
-constexpr uint32_t kOffScale = 0;  // of the tail
-constexpr uint32_t kOffBar = kScaleSlots * kScaleBytes;
-constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;
-constexpr uint32_t kOffAbort = kOffSlot + 8;
-constexpr uint32_t kTailBytes = kOffAbort + 8;
+constexpr int kScaleSlots = 2, kScaleBatch = 4;  // slots of the scales' ring, of so many groups
+// Shared memory: of a CTA that shares its SM with another one; of one that does
+// not. CTAs take no less than kSmemLeast: beside a CTA pair of linear_split (144
+// KB or more) an SM has no room for another that allocates TMEM.
+constexpr uint32_t kSmemHalf = 114688, kSmemAll = 232448, kSmemLeast = 98304;
 constexpr uint32_t kPitch = kP * 4;  // bytes per token of the partial sums
+
+// A kernel for up to 32 kChunks tokens a tile: a sums' warp has every other 16 of
+// them.
+template <int kChunks>
+struct Split {
+  static constexpr bool kShared = kChunks <= 2;  // two CTAs an SM
+  static constexpr int kQ = 32 * kChunks;
+  static constexpr int kBufs = kChunks <= 4 ? 4 : 2;  // accumulators
+  static constexpr uint32_t kScaleBytes = 2 * kQ * 4;  // a group: per token, twice for SwiGLU
+  static constexpr int kFull = 0, kEmpty = kMaxStages, kAccFull = 2 * kMaxStages;
+  static constexpr int kAccEmpty = kAccFull + kBufs, kScFull = kAccEmpty + kBufs;
+  static constexpr int kScEmpty = kScFull + kScaleSlots, kDone = kScEmpty + kScaleSlots;
+  static constexpr int kRecv = kDone + 1, kNumBars = kRecv + 1;
+  static constexpr uint32_t kOffBar = kScaleSlots * kScaleBatch * kScaleBytes;  // of the tail
+  static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;
+  static constexpr uint32_t kOffAbort = kOffSlot + 8;
+  static constexpr uint32_t kTailBytes = kOffAbort + 8;
+  static constexpr uint32_t kSmemMax = kShared ? kSmemHalf : kSmemAll;
+};
 
 struct SplitShape {
   int64_t N, o_bs, o_rs, r_bs, r_rs, xs_bs, xs_rs, xs_ks, ws_rs, ws_ks;
@@ -82,20 +88,23 @@ __device__ __forceinline__ void add4(float4 &v, float4 a) {
   v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
 }
 
-template <int kAct>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int kAct, int kChunks>
+__global__ void __launch_bounds__(kThreads, Split<kChunks>::kShared ? 2 : 1)
     linear_fp8_split_kernel(const __grid_constant__ SplitMaps maps, const SplitShape p,
                             const LinearEpilogue epi, const uint16_t *residual, uint16_t *out,
                             int *status) {
   constexpr bool kGlu = kAct == FLUX_ACT_SWIGLU;
+  using T = Split<kChunks>;
   extern __shared__ __align__(1024) uint8_t base[];
   const uint32_t sbase = smem_addr(base);
   const uint32_t stage_bytes = kPBytes + static_cast<uint32_t>(p.Q) * kGroupK;
   const uint32_t tail = sbase + p.tail;
-  auto bar = [&](int i) { return tail + kOffBar + 8u * static_cast<uint32_t>(i); };
-  auto sc_slot = [&](int i) { return tail + kOffScale + kScaleBytes * static_cast<uint32_t>(i); };
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + p.tail + kOffSlot);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(base + p.tail + kOffAbort);
+  auto bar = [&](int i) { return tail + T::kOffBar + 8u * static_cast<uint32_t>(i); };
+  auto scales_at = [&](int i) {  // group i of the ring's slots
+    return tail + T::kScaleBytes * static_cast<uint32_t>(i);
+  };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + p.tail + T::kOffSlot);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(base + p.tail + T::kOffAbort);
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5;
   const int lane = tid & 31;
@@ -113,21 +122,21 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (tid == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(bar(kBarFull + s), 1);
-      mbar_init(bar(kBarEmpty + s), 1);
+      mbar_init(bar(T::kFull + s), 1);
+      mbar_init(bar(T::kEmpty + s), 1);
     }
-    for (int i = 0; i < kBufs; ++i) {
-      mbar_init(bar(kBarAccFull + i), 1);
-      mbar_init(bar(kBarAccEmpty + i), kSumWarps);
+    for (int i = 0; i < T::kBufs; ++i) {
+      mbar_init(bar(T::kAccFull + i), 1);
+      mbar_init(bar(T::kAccEmpty + i), kSumWarps);
     }
     for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(bar(kBarScFull + i), 1);
-      mbar_init(bar(kBarScEmpty + i), kSumWarps);
+      mbar_init(bar(T::kScFull + i), 1);
+      mbar_init(bar(T::kScEmpty + i), kSumWarps);
     }
-    mbar_init(bar(kBarDone), 1);
-    mbar_init(bar(kBarRecv), 1);
+    mbar_init(bar(T::kDone), 1);
+    mbar_init(bar(T::kRecv), 1);
     if (p.C > 1)
-      mbar_arrive_expect_tx(bar(kBarRecv),
+      mbar_arrive_expect_tx(bar(T::kRecv),
                             static_cast<uint32_t>((p.C - 1) * (row_hi - row_lo)) * kPitch);
     *abort_flag = 0;
     fence_mbar_init();
@@ -165,31 +174,35 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (row != gate_row) gate_raw = load_raw4(epi.gate, row * epi.gate_bs + f, epi.vec_f32);
     gate_row = row;
   };
-  if (mine && epi.bias != nullptr) {
-    bias_raw = load_raw4(epi.bias, f, epi.vec_f32);
-    if constexpr (kGlu) bias_u_raw = load_raw4(epi.bias, p.N + f, epi.vec_f32);
-  }
-  if (mine && epi.gate != nullptr && r < row_hi && s0 + r < p.S) load_gate(s0 + r);
+  auto load_vectors = [&] {
+    if (mine && epi.bias != nullptr) {
+      bias_raw = load_raw4(epi.bias, f, epi.vec_f32);
+      if constexpr (kGlu) bias_u_raw = load_raw4(epi.bias, p.N + f, epi.vec_f32);
+    }
+    if (mine && epi.gate != nullptr && r < row_hi && s0 + r < p.S) load_gate(s0 + r);
+  };
+  // (the sums of larger tiles leave no registers for them)
+  if constexpr (T::kShared) load_vectors();
 
-  float acc[kMaxQ / 32][16];
+  uint64_t acc[kChunks][8];  // pairs of sums
 #pragma unroll
-  for (int i = 0; i < kMaxQ / 32; ++i)
+  for (int i = 0; i < kChunks; ++i)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0;
 
   if (warp == 0 && lane == 0) {
     bool ok = true;
     int s = 0;
     uint32_t turn = 0;
     for (int g = k_lo; g < k_hi; ++g) {
-      if (!(ok = mbar_wait(bar(kBarEmpty + s), (turn & 1u) ^ 1u, abort_flag))) break;
+      if (!(ok = mbar_wait(bar(T::kEmpty + s), (turn & 1u) ^ 1u, abort_flag))) break;
       const uint32_t dst = sbase + static_cast<uint32_t>(s) * stage_bytes;
-      mbar_arrive_expect_tx(bar(kBarFull + s), stage_bytes);
-      tma_load_3d(dst, &maps.w, bar(kBarFull + s), g * kGroupK, static_cast<int>(f0), 0);
+      mbar_arrive_expect_tx(bar(T::kFull + s), stage_bytes);
+      tma_load_3d(dst, &maps.w, bar(T::kFull + s), g * kGroupK, static_cast<int>(f0), 0);
       if constexpr (kGlu)
-        tma_load_3d(dst + kPBytes / 2, &maps.w, bar(kBarFull + s), g * kGroupK,
+        tma_load_3d(dst + kPBytes / 2, &maps.w, bar(T::kFull + s), g * kGroupK,
                     static_cast<int>(p.N + f0), 0);
-      tma_load_3d(dst + kPBytes, &maps.x, bar(kBarFull + s), g * kGroupK, s0, b0);
+      tma_load_3d(dst + kPBytes, &maps.x, bar(T::kFull + s), g * kGroupK, s0, b0);
       if (++s == p.stages) s = 0, ++turn;
     }
     // every copy has landed before the ring is used for the sums
@@ -197,9 +210,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = 0; i < p.stages; ++i) {
       // the stage's last use, if any, was in this turn or the one before
       if (i < s)
-        ok &= mbar_settled(bar(kBarFull + i), turn & 1u, until);
+        ok &= mbar_settled(bar(T::kFull + i), turn & 1u, until);
       else if (turn > 0)
-        ok &= mbar_settled(bar(kBarFull + i), (turn - 1) & 1u, until);
+        ok &= mbar_settled(bar(T::kFull + i), (turn - 1) & 1u, until);
     }
     if (!ok) *abort_flag = 1;
   } else if (warp == 1) {
@@ -207,9 +220,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     int s = 0, buf = 0;
     uint32_t turn = 0, use = 0;  // times round the stages, the accumulators
     for (int g = k_lo; g < k_hi; ++g) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarAccEmpty + buf), (use & 1u) ^ 1u, abort_flag)))
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(T::kAccEmpty + buf), (use & 1u) ^ 1u, abort_flag)))
         break;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarFull + s), turn & 1u, abort_flag))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(T::kFull + s), turn & 1u, abort_flag))) break;
       tc_fence_after_sync();
       const uint32_t st = sbase + static_cast<uint32_t>(s) * stage_bytes;
       const uint64_t da = sdesc_sw128(st, 16, 1024);
@@ -219,12 +232,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int kk = 0; kk < kGroupK / 32; ++kk)
         mma_f8_elect(d, desc_advance(da, kk * 32), desc_advance(db, kk * 32), idesc,
                      kk != 0 ? 1u : 0u);
-      mma_commit_elect(bar(kBarEmpty + s));
-      mma_commit_elect(bar(kBarAccFull + buf));
+      mma_commit_elect(bar(T::kEmpty + s));
+      mma_commit_elect(bar(T::kAccFull + buf));
       if (++s == p.stages) s = 0, ++turn;
-      if (++buf == kBufs) buf = 0, ++use;
+      if (++buf == T::kBufs) buf = 0, ++use;
     }
-    mma_commit_elect(bar(kBarDone));
+    mma_commit_elect(bar(T::kDone));
   } else if (warp == 3) {
     // lanes take the tokens lane, lane + 32, ...; rows of W: one block of 128
     // (for SwiGLU one of the gate rows and one of the linear rows)
@@ -235,95 +248,102 @@ __global__ void __launch_bounds__(kThreads, 2)
     int slot = 0;
     uint32_t use = 0;
     for (int g0 = k_lo; ok && g0 < k_hi; g0 += kScaleBatch) {
-      float x[kScaleBatch][kMaxQ / 32], w0[kScaleBatch], w1[kScaleBatch];
+      float x[kScaleBatch][kChunks], w0[kScaleBatch], w1[kScaleBatch];
 #pragma unroll
       for (int i = 0; i < kScaleBatch; ++i) {
         const int g = g0 + i < k_hi ? g0 + i : k_hi - 1;
         w0[i] = ws0[g * p.ws_ks];
         if constexpr (kGlu) w1[i] = ws1[g * p.ws_ks];
 #pragma unroll
-        for (int j = 0; j < kMaxQ / 32; ++j) {
+        for (int j = 0; j < kChunks; ++j) {
           const int t = j * 32 + lane;
           x[i][j] = t < p.Q && s0 + t < p.S ? xs[(s0 + t) * p.xs_rs + g * p.xs_ks] : 0.f;
         }
       }
+      if (!(ok = __all_sync(0xffffffffu,
+                            mbar_wait(bar(T::kScEmpty + slot), (use & 1u) ^ 1u, abort_flag))))
+        break;
 #pragma unroll
       for (int i = 0; i < kScaleBatch; ++i) {
-        if (g0 + i >= k_hi) break;
-        if (!(ok = __all_sync(0xffffffffu,
-                              mbar_wait(bar(kBarScEmpty + slot), (use & 1u) ^ 1u, abort_flag))))
-          break;
 #pragma unroll
-        for (int j = 0; j < kMaxQ / 32; ++j) {
-          const uint32_t at = sc_slot(slot) + static_cast<uint32_t>(j * 32 + lane) * 4;
-          if (j * 32 >= p.Q) continue;
+        for (int j = 0; j < kChunks; ++j) {
+          const uint32_t at = scales_at(slot * kScaleBatch + i) + static_cast<uint32_t>(j * 32 + lane) * 4;
           st_shared_b32(at, __float_as_uint(x[i][j] * w0[i]));
-          if constexpr (kGlu) st_shared_b32(at + kMaxQ * 4, __float_as_uint(x[i][j] * w1[i]));
+          if constexpr (kGlu) st_shared_b32(at + T::kQ * 4, __float_as_uint(x[i][j] * w1[i]));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarScFull + slot));
-        if (++slot == kScaleSlots) slot = 0, ++use;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(T::kScFull + slot));
+      if (++slot == kScaleSlots) slot = 0, ++use;
     }
   } else if (warp >= 4) {
     const int turn = (warp - 4) >> 2;  // takes the 16-token columns of this parity
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     // the linear rows of a SwiGLU tile are its rows from 64 on
-    const uint32_t sc_off = kGlu && (warp & 3) >= 2 ? kMaxQ * 4 : 0;
+    const uint32_t sc_off = kGlu && (warp & 3) >= 2 ? T::kQ * 4 : 0;
     int buf = 0, slot = 0;
     uint32_t use = 0, sc_use = 0;
+    bool ready = false;  // the next accumulator was complete when last looked at
     for (int g = k_lo; g < k_hi; ++g) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarScFull + slot), sc_use & 1u, abort_flag)))
+      const int in_slot = (g - k_lo) % kScaleBatch;
+      if (in_slot == 0 && !__all_sync(0xffffffffu, mbar_wait(bar(T::kScFull + slot), sc_use & 1u,
+                                                             abort_flag)))
         break;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(kBarAccFull + buf), use & 1u, abort_flag))) break;
+      if (!__all_sync(0xffffffffu, ready) &&
+          !__all_sync(0xffffffffu, mbar_wait(bar(T::kAccFull + buf), use & 1u, abort_flag)))
+        break;
+      const uint32_t scales = scales_at(slot * kScaleBatch + in_slot) + sc_off;
+      const int next = buf + 1 == T::kBufs ? 0 : buf + 1;
+      const uint32_t next_use = next == 0 ? use + 1 : use;
       tc_fence_after_sync();
       const uint32_t from = tmem + static_cast<uint32_t>(buf * p.Q) + lane_off;
+      if (turn * 16 < p.Q) {
 #pragma unroll
-      for (int i = 0; i < kMaxQ / 32; ++i) {
-        const int c = (2 * i + turn) * 16;
-        if (c >= p.Q) break;
-        uint32_t v[16];
-        tmem_ld16(from + static_cast<uint32_t>(c), v);
-        float4 sc[4];
+        for (int i = 0; i < kChunks; ++i) {
+          const uint32_t c = static_cast<uint32_t>((2 * i + turn) * 16);
+          uint64_t v[8];
+          tmem_ld16_pairs(from + c, v);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          sc[j] = ld_shared_f4(sc_slot(slot) + sc_off + static_cast<uint32_t>(c * 4 + j * 16));
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[i][4 * j] = fmaf(__uint_as_float(v[4 * j]), sc[j].x, acc[i][4 * j]);
-          acc[i][4 * j + 1] = fmaf(__uint_as_float(v[4 * j + 1]), sc[j].y, acc[i][4 * j + 1]);
-          acc[i][4 * j + 2] = fmaf(__uint_as_float(v[4 * j + 2]), sc[j].z, acc[i][4 * j + 2]);
-          acc[i][4 * j + 3] = fmaf(__uint_as_float(v[4 * j + 3]), sc[j].w, acc[i][4 * j + 3]);
+          for (int j = 0; j < 4; ++j) {
+            const uint4 sc = ld_shared_v4(scales + c * 4 + j * 16);
+            const uint64_t s0 = f2_pack(__uint_as_float(sc.x), __uint_as_float(sc.y));
+            const uint64_t s1 = f2_pack(__uint_as_float(sc.z), __uint_as_float(sc.w));
+            acc[i][2 * j] = f2_fma(v[2 * j], s0, acc[i][2 * j]);
+            acc[i][2 * j + 1] = f2_fma(v[2 * j + 1], s1, acc[i][2 * j + 1]);
+          }
         }
       }
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(kBarAccEmpty + buf));
-        mbar_arrive(bar(kBarScEmpty + slot));
+      if (lane == 0) mbar_arrive(bar(T::kAccEmpty + buf));
+      ready = mbar_test_wait(bar(T::kAccFull + next), next_use & 1u);
+      if (in_slot == kScaleBatch - 1 || g == k_hi - 1) {
+        if (lane == 0) mbar_arrive(bar(T::kScEmpty + slot));
+        if (++slot == kScaleSlots) slot = 0, ++sc_use;
       }
-      if (++buf == kBufs) buf = 0, ++use;
-      if (++slot == kScaleSlots) slot = 0, ++sc_use;
+      buf = next, use = next_use;
     }
   }
   __syncwarp();
   // The MMAs have read the ring, an aborted CTA's too: its issuer commits them
   // when its own wait has run out, so that this one is longer.
-  if (!mbar_settled(bar(kBarDone), 0, clock64() + 3 * kWaitBudgetCycles)) *abort_flag = 1;
+  if (!mbar_settled(bar(T::kDone), 0, clock64() + 3 * kWaitBudgetCycles)) *abort_flag = 1;
   __syncthreads();
   if (warp >= 4) {
     // one row of W per thread: consecutive lanes write consecutive words
     const int turn = (warp - 4) >> 2;
     const uint32_t row = static_cast<uint32_t>((warp & 3) * 32 + lane);
 #pragma unroll
-    for (int i = 0; i < kMaxQ / 32; ++i) {
-      const int c = (2 * i + turn) * 16;
-      if (c >= p.Q) break;
+    for (int i = 0; i < kChunks; ++i) {
+      if (turn * 16 >= p.Q) break;
+      const uint32_t at = sbase + static_cast<uint32_t>((2 * i + turn) * 16) * kPitch + row * 4;
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        st_shared_b32(sbase + static_cast<uint32_t>(c + j) * kPitch + row * 4,
-                      __float_as_uint(acc[i][j]));
+      for (int j = 0; j < 8; ++j) {
+        float a, b;
+        f2_unpack(acc[i][j], a, b);
+        st_shared_b32(at + (2 * j) * kPitch, __float_as_uint(a));
+        st_shared_b32(at + (2 * j + 1) * kPitch, __float_as_uint(b));
+      }
     }
   }
   fence_proxy_async_smem();
@@ -339,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       v = *reinterpret_cast<const uint2 *>(residual + b0 * p.r_bs + (s0 + row) * p.r_rs + f);
     return v;
   };
+  if constexpr (!T::kShared) load_vectors();
   uint2 res = fetch(r), res1 = fetch(r + per);
   if (p.C > 1) {
     // a warp per other CTA sends that one's rows, in four copies
@@ -351,14 +372,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             mapa_shared(sbase + p.recv + static_cast<uint32_t>(
                             (part < warp ? part : part - 1) * n + q_lo) * kPitch, to),
             sbase + static_cast<uint32_t>(lo + q_lo) * kPitch,
-            static_cast<uint32_t>(q_n) * kPitch, mapa_shared(bar(kBarRecv), to));
+            static_cast<uint32_t>(q_n) * kPitch, mapa_shared(bar(T::kRecv), to));
     }
     __syncwarp();
     // An abort does not end this wait: every CTA sends its rows, an aborted one
     // too, and they must have arrived before this one lets the cluster go. The
     // last may have waited for its MMAs for three budgets since this one was done.
-    if (!mbar_try_wait_cluster(bar(kBarRecv), 0) &&
-        !mbar_settled(bar(kBarRecv), 0, clock64() + 4 * kWaitBudgetCycles))
+    if (!mbar_try_wait_cluster(bar(T::kRecv), 0) &&
+        !mbar_settled(bar(T::kRecv), 0, clock64() + 4 * kWaitBudgetCycles))
       *abort_flag = 1;
   }
   __syncwarp();
@@ -417,19 +438,23 @@ uint32_t recv_bytes(int Q, int C) {
   return static_cast<uint32_t>((C - 1) * ((Q + C - 1) / C)) * kPitch;
 }
 
-template <int kAct>
+// A tile's tokens: 16, 32, 64, 96, 128 or 192.
+int chunks_of(int Q) { return (Q + 31) / 32; }
+
+template <int kAct, int kChunks>
 cudaError_t launch(const LinearFp8Problem &q, const Fp8SplitPlan &plan, const LinearEpilogue &epi,
                    int *status, cudaStream_t stream) {
+  using T = Split<kChunks>;
   static std::once_flag attr_once[64];
   static cudaError_t attr_err[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  auto kernel = linear_fp8_split_kernel<kAct>;
+  auto kernel = linear_fp8_split_kernel<kAct, kChunks>;
   std::call_once(attr_once[dev], [&] {
     attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kSmemHalf));
+                                         static_cast<int>(T::kSmemMax));
   });
   if (attr_err[dev] != cudaSuccess) return attr_err[dev];
   constexpr bool glu = kAct == FLUX_ACT_SWIGLU;
@@ -448,15 +473,16 @@ cudaError_t launch(const LinearFp8Problem &q, const Fp8SplitPlan &plan, const Li
   p.n_tb = static_cast<int>(n_sb * q.B);
   p.nk = (q.K + kGroupK - 1) / kGroupK;
   p.tmem_cols = 32;
-  while (p.tmem_cols < kBufs * p.Q) p.tmem_cols *= 2;
+  while (p.tmem_cols < T::kBufs * p.Q) p.tmem_cols *= 2;
   // the CTA's own partial sums over the drained ring, the others' behind them
   const uint32_t ring = static_cast<uint32_t>(p.stages) * stage_size(p.Q);
   const uint32_t own = own_bytes(p.Q), recv = recv_bytes(p.Q, p.C);
   p.early = plan.early ? 1 : 0;
   p.recv = plan.early ? std::max(ring, own) : own;
   p.tail = (std::max(ring, p.recv + recv) + 127) & ~127u;
-  const uint32_t smem = std::max(p.tail + kTailBytes, kSmemLeast);
-  if (smem > kSmemHalf || p.C > p.nk || p.C > kMaxUnits || p.Q > kMaxQ) return cudaErrorInvalidValue;
+  const uint32_t smem = std::max(p.tail + T::kTailBytes, kSmemLeast);
+  if (smem > T::kSmemMax || p.C > p.nk || p.C > kMaxUnits || chunks_of(p.Q) != kChunks)
+    return cudaErrorInvalidValue;
   const int64_t wr = glu ? 2 * q.N : q.N;
   SplitMaps maps;
   if (!make_byte_map(&maps.x, q.x, q.K, q.S, q.B, q.x_rs, q.x_bs, static_cast<uint32_t>(p.Q)) ||
@@ -482,6 +508,26 @@ cudaError_t launch(const LinearFp8Problem &q, const Fp8SplitPlan &plan, const Li
                             static_cast<uint16_t *>(q.out), status);
 }
 
+template <int kAct>
+cudaError_t launch(const LinearFp8Problem &q, const Fp8SplitPlan &plan, const LinearEpilogue &epi,
+                   int *status, cudaStream_t stream) {
+  switch (chunks_of(plan.Q)) {
+    case 1: return launch<kAct, 1>(q, plan, epi, status, stream);
+    case 2: return launch<kAct, 2>(q, plan, epi, status, stream);
+    case 3: return launch<kAct, 3>(q, plan, epi, status, stream);
+    case 4: return launch<kAct, 4>(q, plan, epi, status, stream);
+    case 6: return launch<kAct, 6>(q, plan, epi, status, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+uint32_t tail_bytes(int Q) {
+  const int c = chunks_of(Q);
+  return c == 1 ? Split<1>::kTailBytes : c == 2 ? Split<2>::kTailBytes
+         : c == 3 ? Split<3>::kTailBytes : c == 4 ? Split<4>::kTailBytes
+                  : Split<6>::kTailBytes;
+}
+
 }  // namespace
 
 Fp8SplitPlan plan_fp8_split(const LinearFp8Problem &q, int act, int sms) {
@@ -489,26 +535,46 @@ Fp8SplitPlan plan_fp8_split(const LinearFp8Problem &q, int act, int sms) {
   const int nk = (q.K + kGroupK - 1) / kGroupK;
   const int64_t feats = glu ? kP / 2 : kP, n_ft = (q.N + feats - 1) / feats;
   Fp8SplitPlan best{0, 0, 0, false, 1e30};
-  const uint32_t room = kSmemHalf - kTailBytes - 128;
-  // even shares of a batch element's tokens, as few as there can be and twice that
-  const int64_t fewest = (q.S + kMaxQ - 1) / kMaxQ;
-  for (int64_t n_sb = fewest; n_sb <= 2 * fewest && n_sb <= q.S; n_sb += fewest) {
-    const int Q = static_cast<int>(((q.S + n_sb - 1) / n_sb + 15) / 16 * 16);
+  // Estimates in ns, fitted to 1185 times of these forms at 38 problems of 1 to 512
+  // tokens (with linear_fp8_pair's, the pick takes 1.02 times the best form's time,
+  // geometric mean, 1.2 at most): per wave, group and its column, bytes per ns that
+  // a CTA's stages and sums come at (a CTA that shares its SM at half that), what a
+  // late place for the sums costs, finishing a row.
+  struct Costs {
+    double wave, group, column, bytes, send, late, row;
+  };
+  static constexpr Costs kShared = {3110.0, 148.0, 7.5, 69.0, 14.7, 113.0, 0.0};
+  static constexpr Costs kWhole = {4480.0, 0.0, 3.95, 100.0, 44.0, 0.0, 6.5};
+  static constexpr int kTokens[] = {16, 32, 64, 96, 128, 192};
+  static constexpr int kResident[9] = {0, 152, 152, 147, 144, 140, 138, 0, 120};  // an SM each
+  const int64_t wr = glu ? 2 * q.N : q.N;
+  const double bytes = static_cast<double>(q.B * q.S + wr) * q.K +
+                       2.0 * static_cast<double>(q.B * q.S) * q.N * (q.residual != nullptr ? 2 : 1);
+  for (int Q : kTokens) {
     const int64_t n_tb = q.B * ((q.S + Q - 1) / Q);
-    for (int C = 1; C <= kMaxUnits && C <= nk; C *= 2) {
+    const bool shared = chunks_of(Q) <= 2;
+    const Costs &t = shared ? kShared : kWhole;
+    const uint32_t room = (shared ? kSmemHalf : kSmemAll) - tail_bytes(Q) - 128;
+    for (int C = 1; C <= kMaxUnits && C <= nk; ++C) {
+      const int64_t slots = shared ? 2 * sms : kResident[C] * static_cast<int64_t>(sms) / 152;
       const uint32_t stage = stage_size(Q), recv = recv_bytes(Q, C);
-      if (own_bytes(Q) + recv > room || 3 * stage > room) continue;
-      const bool early = C > 1 && recv <= 16 * 1024;
+      if (slots < C || own_bytes(Q) + recv > room || 3 * stage > room) continue;
+      // a place of their own for the sums saves a cluster barrier, unless the ring
+      // gets short for it
+      const bool early = C > 1 && recv <= 16 * 1024 && recv + 3 * stage <= room;
       const int stages = static_cast<int>(std::min<uint32_t>(
           kMaxStages, (early ? room - recv : room) / stage));
-      const double ctas = static_cast<double>(n_ft) * n_tb * C;
-      const double waves = std::max(1.0, std::ceil(ctas / (2.0 * sms)));
-      const double share = ctas <= sms ? 1.0 : std::min(2.0, ctas / sms);
-      const double per = std::max(stage / kBytesPerNs * share, 150.0 + Q);
-      const double ns = waves * (2500.0 + std::ceil(static_cast<double>(nk) / C) * per) +
-                        (C > 1 ? 800.0 + recv / 30.0 : 0.0) + Q * 8.0;
+      const double ctas = static_cast<double>(n_ft) * static_cast<double>(n_tb) * C;
+      const double waves = std::ceil(ctas / static_cast<double>(slots));
+      const double share = !shared || ctas <= sms ? 1.0 : std::min(2.0, ctas / sms);
+      const double per = std::max(stage / t.bytes * share, t.group + t.column * Q);
+      const double ns =
+          std::max(waves * (t.wave + std::ceil(static_cast<double>(nk) / C) * per),
+                   bytes / 6690.0 + t.wave) +
+          (C > 1 ? recv / t.send + (early ? 0.0 : t.late) : 0.0) + t.row * Q / C;
       if (ns < best.ns) best = Fp8SplitPlan{Q, C, stages, early, ns};
     }
+    if (Q >= q.S) break;
   }
   return best;
 }
