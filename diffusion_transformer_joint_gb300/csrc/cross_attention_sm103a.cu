@@ -44,6 +44,7 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "flux_internal.h"
 #include "ptx_sm103a.cuh"
@@ -56,7 +57,7 @@ constexpr int kThreads = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLowest = -3.0e38f;        // a maximum no key has been counted in
 constexpr uint32_t kBlockBytes = 16384;    // 128 rows x 64 channels, one swizzle block
-constexpr uint32_t kBoxBytes = 32 * 64;    // epilogue: 32 rows x 32 channels
+constexpr uint32_t kBoxBytes = 32 * 128;   // epilogue: 32 rows x 64 channels
 constexpr uint32_t kTmemCols = 512;
 constexpr int kAll = 0, kLengths = 1, kMask = 2;
 constexpr int kMaxParts = 16;  // of the keys: CTAs of a cluster
@@ -72,7 +73,7 @@ struct Layout {
   static constexpr uint32_t kOffK = kQTiles * kTileBytes;
   static constexpr uint32_t kOffV = kOffK + kStages * kTileBytes;
   static constexpr uint32_t kOffBox = kOffV + kStages * kTileBytes;
-  static constexpr uint32_t kOffRow = kOffBox + (kNarrow ? 0 : 4 * (kD / 32) * kBoxBytes);
+  static constexpr uint32_t kOffRow = kOffBox + (kNarrow ? 0 : 4 * (kD / 64) * kBoxBytes);
   static constexpr uint32_t kOffBar = kOffRow + 2 * 2 * kTile * 4;  // (m and l of a stream's rows)
   // barriers
   static constexpr int kQFull = 0, kQFree = 2, kKFull = 4, kKEmpty = kKFull + kStages;
@@ -546,81 +547,97 @@ __global__ void __launch_bounds__(kThreads, 1)
           warp_arrive(bar(L::kPFull + t), lane);
           continue;
         }
-        uint32_t sr[kTile];
-        float mr[4];
+        float alpha = 1.f, sum, m_use = m_run;
+        // kPart: some of the tile's keys take no part. (A tile that they all take
+        // part in has code of its own: with the choice inside it ran a tenth slower.)
+        auto tile = [&](auto part) {
+          constexpr bool kPart = decltype(part)::value;
+          uint32_t sr[kTile];
+          float mr[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_ld32_max(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]), mr[c]);
-        tmem_ld_wait();
-        float mx = fmax3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
-        const bool all = kKeys == kMask
-                             ? (bits[0] & bits[1] & bits[2] & bits[3]) == 0xffffffffu
-                             : it.keys - (it.lo + j) * kTile >= kTile;
-        if (!all) {
-          if constexpr (kKeys != kMask) key_bits(it, j, bits);
-          mx = -INFINITY;
+          for (int c = 0; c < 4; ++c)
+            tmem_ld32_max(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]), mr[c]);
+          tmem_ld_wait();
+          float mx;
+          if constexpr (!kPart) {
+            mx = fmax3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
+          } else {
+            // 32 keys at a time: all of them take part (the loads' maximum holds),
+            // none, or some, whose others' scores are replaced
+            if constexpr (kKeys != kMask) key_bits(it, j, bits);
+            mx = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            float a = -INFINITY, b = -INFINITY;
+            for (int w = 0; w < 4; ++w) {
+              if (bits[w] == 0xffffffffu) {
+                mx = fmaxf(mx, mr[w]);
+              } else if (bits[w] != 0) {
+                float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const int at = w * 32 + e;
-              if (!(bits[w] & (1u << e))) sr[at] = 0xff800000u;
-              if (!(bits[w] & (2u << e))) sr[at + 1] = 0xff800000u;
-              if (e & 2)
-                a = fmax3(a, __uint_as_float(sr[at]), __uint_as_float(sr[at + 1]));
-              else
-                b = fmax3(b, __uint_as_float(sr[at]), __uint_as_float(sr[at + 1]));
+                for (int e = 0; e < 32; e += 2) {
+                  const int at = w * 32 + e;
+                  if (!(bits[w] & (1u << e))) sr[at] = 0xff800000u;
+                  if (!(bits[w] & (2u << e))) sr[at + 1] = 0xff800000u;
+                  if (e & 2)
+                    a = fmax3(a, __uint_as_float(sr[at]), __uint_as_float(sr[at + 1]));
+                  else
+                    b = fmax3(b, __uint_as_float(sr[at]), __uint_as_float(sr[at + 1]));
+                }
+                mx = fmax3(mx, a, b);
+              }
             }
-            mx = fmax3(mx, a, b);
           }
-        }
-        mx = fmaxf(mx * scale_log2, kLowest);  // (no key so far: p is 2^-inf below)
-        float alpha = 1.f;
-        float m_use = m_run;
-        if (fresh) {
-          m_use = mx;
-        } else if (__any_sync(0xffffffffu, mx > m_run + kRescaleThreshold)) {
-          m_use = fmaxf(m_run, mx);
-          alpha = ex2_approx(m_run - m_use);
-          // S_t of this tile is complete, hence so is PV_t before it: O_t is stable
+          mx = fmaxf(mx * scale_log2, kLowest);  // (no key so far: p is 2^-inf below)
+          if (fresh) {
+            m_use = mx;
+          } else if (__any_sync(0xffffffffu, mx > m_run + kRescaleThreshold)) {
+            m_use = fmaxf(m_run, mx);
+            alpha = ex2_approx(m_run - m_use);
+            // S_t of this tile is complete, hence so is PV_t before it: O_t is stable
 #pragma unroll 1
-          for (int c = 0; c < kD / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(tO + c * 16, o);
-            tmem_ld_wait();
+            for (int c = 0; c < kD / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + c * 16, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(tO + c * 16, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(tO + c * 16, o);
+            }
           }
-        }
-        fresh = false;
-        const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
-        const uint64_t negm2 = f2_pack(-m_use, -m_use);
-        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+          const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
+          const uint64_t negm2 = f2_pack(-m_use, -m_use);
+          uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+            if (kPart && bits[c] == 0) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint64_t x2 =
-                f2_pack(__uint_as_float(sr[c * 32 + e]), __uint_as_float(sr[c * 32 + e + 1]));
-            float y0, y1;
-            f2_unpack(f2_fma(x2, scale2, negm2), y0, y1);
-            const float p0 = ex2_approx(y0);
-            const float p1 = ex2_approx(y1);
-            acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
-            pk[e / 2] = pack_bf16x2(p0, p1);
+              for (int e = 0; e < 16; ++e) pk[e] = 0;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const uint64_t x2 =
+                    f2_pack(__uint_as_float(sr[c * 32 + e]), __uint_as_float(sr[c * 32 + e + 1]));
+                float y0, y1;
+                f2_unpack(f2_fma(x2, scale2, negm2), y0, y1);
+                const float p0 = ex2_approx(y0);
+                const float p1 = ex2_approx(y1);
+                acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
+                pk[e / 2] = pack_bf16x2(p0, p1);
+              }
+            }
+            tmem_st16(tS + c * 16, pk);
           }
-          tmem_st16(tS + c * 16, pk);
-        }
-        float sum;
-        {
           float a0, a1, b0, b1;
           f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
           f2_unpack(f2_add(acc[2], acc[3]), b0, b1);
           sum = (a0 + a1) + (b0 + b1);
-        }
+        };
+        if (kKeys == kMask ? (bits[0] & bits[1] & bits[2] & bits[3]) == 0xffffffffu
+                           : it.keys - (it.lo + j) * kTile >= kTile)
+          tile(std::false_type());
+        else
+          tile(std::true_type());
+        fresh = false;
         tmem_st_wait();
         l_run = l_run * alpha + sum;
         m_run = m_use;
@@ -653,61 +670,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t) {
           const int s_tile = it.s0 + t * p.n_s, s = s_tile + qs;
           const bool row_ok = qs < p.n_s && s < p.Sq;
-          float inv_l = 0.f;
-          if (it.n > 0) {
-            if (!(ok = wait_warp(bar(L::kRowFull + t), k & 1u, abort_flag))) break;
-            const float l = ld_shared_f32(row_at(t, 1, row));
-            inv_l = l == 0.f ? 0.f : 1.f / l;
-            warp_arrive(bar(L::kRowFree + t), lane);
-            if (!(ok = wait_warp(bar(L::kODone + t), k & 1u, abort_flag))) break;
-            tc_fence_after_sync();
+          auto row_to = [&] {
+            return p.out + it.b * p.o_bs + static_cast<int64_t>(s) * p.o_rs +
+                   static_cast<int64_t>(it.h * p.G + qh) * kD;
+          };
+          if (it.n <= 0) {  // no keys
+            if (row_ok)
+              for (int q = 0; q < kD / 8; ++q)
+                st_global_v4(row_to() + q * 8, make_uint4(0u, 0u, 0u, 0u));
+            continue;
           }
+          if (!(ok = wait_warp(bar(L::kRowFull + t), k & 1u, abort_flag))) break;
+          const float l = ld_shared_f32(row_at(t, 1, row));
+          const float inv_l = l == 0.f ? 0.f : 1.f / l;
+          warp_arrive(bar(L::kRowFree + t), lane);
+          if (!(ok = wait_warp(bar(L::kODone + t), k & 1u, abort_flag))) break;
+          tc_fence_after_sync();
           // the row's values to registers as bf16, and O is free for the next item
           const uint32_t tO = tmem + 256 + t * 128 + lane_off;
-          uint4 w[kD / 8];
+          const uint64_t inv2 = f2_pack(inv_l, inv_l);
+          uint32_t w[kD / 2];
 #pragma unroll
-          for (int c = 0; c < kD / 32; ++c) {
-            uint32_t o[32];
-            if (it.n > 0) {
-              tmem_ld32(tO + c * 32, o);
-              tmem_ld_wait();
-            }
+          for (int c = 0; c < kD / 16; ++c) {
+            uint64_t o[8];
+            tmem_ld16_pairs(tO + c * 16, o);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              auto v = [&](int e) {
-                return it.n > 0 ? __uint_as_float(o[8 * q + e]) * inv_l : 0.f;
-              };
-              w[c * 4 + q] = make_uint4(pack_bf16x2(v(0), v(1)), pack_bf16x2(v(2), v(3)),
-                                        pack_bf16x2(v(4), v(5)), pack_bf16x2(v(6), v(7)));
+            for (int e = 0; e < 8; ++e) {
+              float x, y;
+              f2_unpack(f2_mul(o[e], inv2), x, y);
+              w[c * 8 + e] = pack_bf16x2(x, y);
             }
           }
-          if (it.n > 0) {
-            tc_fence_before_sync();
-            warp_arrive(bar(L::kOFree + t), lane);
-          }
+          tc_fence_before_sync();
+          warp_arrive(bar(L::kOFree + t), lane);
           if (p.boxed) {
+            // boxes of 64 channels, a row's 16-byte chunks swizzled over 128 bytes
             const uint32_t boxes = sbase + L::kOffBox +
-                                   static_cast<uint32_t>((warp - 12) * (kD / 32)) * kBoxBytes;
+                                   static_cast<uint32_t>((warp - 12) * (kD / 64)) * kBoxBytes;
             const int box_s = s_tile + wq * 32 / p.G;  // first query of the warp's boxes
             if (lane == 0) bulk_wait_read_all();  // the copies before have read the boxes
             __syncwarp();
 #pragma unroll
             for (int q = 0; q < kD / 8; ++q)
-              st_shared_v4(boxes + (q >> 2) * kBoxBytes + lane * 64 +
-                               (((q & 3) ^ ((lane >> 1) & 3)) << 4),
-                           w[q]);
+              st_shared_v4(boxes + (q >> 3) * kBoxBytes + lane * 128 + (((q ^ lane) & 7) << 4),
+                           make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && box_s < p.Sq) {
-              for (int c = 0; c < kD / 32; ++c)
-                tma_store_5d(&maps.out, boxes + c * kBoxBytes, c * 32, 0, it.h, box_s, it.b);
+              for (int c = 0; c < kD / 64; ++c)
+                tma_store_5d(&maps.out, boxes + c * kBoxBytes, c * 64, 0, it.h, box_s, it.b);
               bulk_commit();
             }
           } else if (row_ok) {
-            uint16_t *to = p.out + it.b * p.o_bs + static_cast<int64_t>(s) * p.o_rs +
-                           static_cast<int64_t>(it.h * p.G + qh) * kD;
+            uint16_t *to = row_to();
 #pragma unroll
-            for (int q = 0; q < kD / 8; ++q) st_global_v4(to + q * 8, w[q]);
+            for (int q = 0; q < kD / 8; ++q)
+              st_global_v4(to + q * 8, make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
           }
         }
         if (!ok) break;
@@ -835,10 +853,11 @@ using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, vo
                               const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// Heads [B, S, Hk, G, D] as (D, G, Hk, S, B); a box is box_ch channels (a
-// swizzled row of 128 or 64 bytes) of the G heads of box_s tokens.
+// Heads [B, S, Hk, G, D] as (D, G, Hk, S, B), or [B, S, Hk, D] as (D, Hk, S, B)
+// with G = 0; a box is 64 channels (a swizzled row of 128 bytes) of the G heads of
+// box_s tokens.
 bool make_map(CUtensorMap *map, const void *x, int D, int G, int Hk, int64_t S, int64_t B,
-              int64_t rs, int64_t bs, uint32_t box_ch, uint32_t box_s, bool grouped) {
+              int64_t rs, int64_t bs, uint32_t box_s) {
   auto fn = reinterpret_cast<EncodeFn>(tensor_map_encode_entry());
   if (fn == nullptr) return false;
   cuuint64_t dims[5], strides[4];
@@ -849,14 +868,13 @@ bool make_map(CUtensorMap *map, const void *x, int D, int G, int Hk, int64_t S, 
     if (n > 0) strides[n - 1] = static_cast<cuuint64_t>(step) * 2;
     box[n++] = b;
   };
-  axis(D, 1, box_ch);
-  if (grouped) axis(G, D, static_cast<uint32_t>(G));
-  axis(Hk, static_cast<int64_t>(G) * D, 1);
+  axis(D, 1, 64);
+  if (G > 0) axis(G, D, static_cast<uint32_t>(G));
+  axis(Hk, static_cast<int64_t>(G > 0 ? G : 1) * D, 1);
   axis(S, rs, box_s);
   axis(B, bs, 1);
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(n), const_cast<void *>(x),
-            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_ch == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -893,15 +911,15 @@ cudaError_t launch(const CrossAttention &a, const CrossPlan &plan, int sms, int 
   p.boxed = 32 % p.G == 0 ? 1 : 0;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   Maps maps;
-  if (!make_map(&maps.q, a.q, kD, p.G, a.Hk, a.Sq, a.B, a.q_rs, a.q_bs, 64,
-                static_cast<uint32_t>(p.n_s), true) ||
-      !make_map(&maps.k, a.k, kD, 1, a.Hk, a.Sk, a.B, a.k_rs, a.k_bs, 64, kTile, false) ||
-      !make_map(&maps.v, a.v, kD, 1, a.Hk, a.Sk, a.B, a.v_rs, a.v_bs, 64, kTile, false))
+  if (!make_map(&maps.q, a.q, kD, p.G, a.Hk, a.Sq, a.B, a.q_rs, a.q_bs,
+                static_cast<uint32_t>(p.n_s)) ||
+      !make_map(&maps.k, a.k, kD, 0, a.Hk, a.Sk, a.B, a.k_rs, a.k_bs, kTile) ||
+      !make_map(&maps.v, a.v, kD, 0, a.Hk, a.Sk, a.B, a.v_rs, a.v_bs, kTile))
     return cudaErrorInvalidValue;
   maps.out = maps.q;  // (not looked at where rows are stored one by one)
   if (!kNarrow && p.boxed &&
-      !make_map(&maps.out, a.out, kD, p.G, a.Hk, a.Sq, a.B, a.o_rs, a.o_bs, 32,
-                static_cast<uint32_t>(32 / p.G), true))
+      !make_map(&maps.out, a.out, kD, p.G, a.Hk, a.Sq, a.B, a.o_rs, a.o_bs,
+                static_cast<uint32_t>(32 / p.G)))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
