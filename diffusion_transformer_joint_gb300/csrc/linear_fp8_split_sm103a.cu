@@ -1,5 +1,5 @@
 // flux_linear_fp8 where whole 256-row tiles would leave SMs idle (few tokens, or
-// few features), on sm_103a (GB300): tiles of 128 rows of W against up to 192
+// few features), on sm_103a (GB300): tiles of 128 rows of W against up to 128
 // tokens, the channels split over a cluster.
 //
 //   y[t, n] = sum_g xs[t, g] ws[n / 128, g] sum_{k in g} x[t, k] w[n, k]
@@ -10,9 +10,9 @@
 // A pipeline stage is one group of 128 channels. Its four K32 MMAs start a
 // fresh accumulator; eight warps read it, multiply each token's column with
 // xs[t, g] * ws[.., g] and add it to fp32 sums in registers, while the MMAs of
-// the next groups fill the other accumulators (four, or two of over 128 columns):
-// the products inside a group are summed by the tensor core in fp32, the groups
-// by fp32 FMAs in the order of the channels.
+// the next groups fill the other three accumulators: the products inside a group
+// are summed by the tensor core in fp32, the groups by fp32 FMAs in the order of
+// the channels.
 //
 // As linear_split, the groups of a tile are split over the C CTAs of a cluster
 // (an SM takes in about 110 bytes per ns, whatever the tile computes), which send
@@ -55,7 +55,7 @@ template <int kChunks>
 struct Split {
   static constexpr bool kShared = kChunks <= 2;  // two CTAs an SM
   static constexpr int kQ = 32 * kChunks;
-  static constexpr int kBufs = kChunks <= 4 ? 4 : 2;  // accumulators
+  static constexpr int kBufs = 4;  // accumulators
   static constexpr uint32_t kScaleBytes = 2 * kQ * 4;  // a group: per token, twice for SwiGLU
   static constexpr int kFull = 0, kEmpty = kMaxStages, kAccFull = 2 * kMaxStages;
   static constexpr int kAccEmpty = kAccFull + kBufs, kScFull = kAccEmpty + kBufs;
@@ -438,7 +438,7 @@ uint32_t recv_bytes(int Q, int C) {
   return static_cast<uint32_t>((C - 1) * ((Q + C - 1) / C)) * kPitch;
 }
 
-// A tile's tokens: 16, 32, 64, 96, 128 or 192.
+// A tile's tokens: 16, 32, 64, 96 or 128.
 int chunks_of(int Q) { return (Q + 31) / 32; }
 
 template <int kAct, int kChunks>
@@ -516,7 +516,6 @@ cudaError_t launch(const LinearFp8Problem &q, const Fp8SplitPlan &plan, const Li
     case 2: return launch<kAct, 2>(q, plan, epi, status, stream);
     case 3: return launch<kAct, 3>(q, plan, epi, status, stream);
     case 4: return launch<kAct, 4>(q, plan, epi, status, stream);
-    case 6: return launch<kAct, 6>(q, plan, epi, status, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -524,8 +523,7 @@ cudaError_t launch(const LinearFp8Problem &q, const Fp8SplitPlan &plan, const Li
 uint32_t tail_bytes(int Q) {
   const int c = chunks_of(Q);
   return c == 1 ? Split<1>::kTailBytes : c == 2 ? Split<2>::kTailBytes
-         : c == 3 ? Split<3>::kTailBytes : c == 4 ? Split<4>::kTailBytes
-                  : Split<6>::kTailBytes;
+         : c == 3 ? Split<3>::kTailBytes : Split<4>::kTailBytes;
 }
 
 }  // namespace
@@ -535,7 +533,7 @@ Fp8SplitPlan plan_fp8_split(const LinearFp8Problem &q, int act, int sms) {
   const int nk = (q.K + kGroupK - 1) / kGroupK;
   const int64_t feats = glu ? kP / 2 : kP, n_ft = (q.N + feats - 1) / feats;
   Fp8SplitPlan best{0, 0, 0, false, 1e30};
-  // Estimates in ns, fitted to 1185 times of these forms at 38 problems of 1 to 512
+  // Estimates in ns, fitted to the times of these forms at 38 problems of 1 to 512
   // tokens (with linear_fp8_pair's, the pick takes 1.02 times the best form's time,
   // geometric mean, 1.2 at most): per wave, group and its column, bytes per ns that
   // a CTA's stages and sums come at (a CTA that shares its SM at half that), what a
@@ -545,7 +543,7 @@ Fp8SplitPlan plan_fp8_split(const LinearFp8Problem &q, int act, int sms) {
   };
   static constexpr Costs kShared = {3110.0, 148.0, 7.5, 69.0, 14.7, 113.0, 0.0};
   static constexpr Costs kWhole = {4480.0, 0.0, 3.95, 100.0, 44.0, 0.0, 6.5};
-  static constexpr int kTokens[] = {16, 32, 64, 96, 128, 192};
+  static constexpr int kTokens[] = {16, 32, 64, 96, 128};
   static constexpr int kResident[9] = {0, 152, 152, 147, 144, 140, 138, 0, 120};  // an SM each
   const int64_t wr = glu ? 2 * q.N : q.N;
   const double bytes = static_cast<double>(q.B * q.S + wr) * q.K +
@@ -555,7 +553,7 @@ Fp8SplitPlan plan_fp8_split(const LinearFp8Problem &q, int act, int sms) {
     const bool shared = chunks_of(Q) <= 2;
     const Costs &t = shared ? kShared : kWhole;
     const uint32_t room = (shared ? kSmemHalf : kSmemAll) - tail_bytes(Q) - 128;
-    for (int C = 1; C <= kMaxUnits && C <= nk; ++C) {
+    for (int C = 1; C <= kMaxUnits && C <= nk; C += C == 6 ? 2 : 1) {
       const int64_t slots = shared ? 2 * sms : kResident[C] * static_cast<int64_t>(sms) / 152;
       const uint32_t stage = stage_size(Q), recv = recv_bytes(Q, C);
       if (slots < C || own_bytes(Q) + recv > room || 3 * stage > room) continue;
