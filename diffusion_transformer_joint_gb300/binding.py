@@ -45,6 +45,25 @@ class FluxError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_compiled = None  # the compiled marshalling, and the library that it calls
+_compiled_lib = None
+
+
+def _load_compiled(lib):
+    """The compiled marshalling (build.build_marshal) of the calls that have one, over
+    `lib`; without it they are marshalled here."""
+    global _compiled, _compiled_lib
+    path = _build.marshal_path()
+    if not os.path.exists(path):
+        return
+    import importlib.util
+
+    spec = importlib.util.spec_from_file_location("_marshal", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
+                  ("flux_quantize_fp8", "flux_linear_fp8", "flux_cross_attention")))
+    _compiled, _compiled_lib = module, lib
 
 
 def library_path() -> str:
@@ -146,6 +165,7 @@ def load(path: str | None = None):
             lib.flux_take_status.restype = I32
             lib.flux_status_string.argtypes = [I32]
             lib.flux_status_string.restype = ctypes.c_char_p
+            _load_compiled(lib)
             _lib = lib
     return _lib
 
@@ -845,6 +865,13 @@ def modulated_norm(x, scale=None, shift=None, y=None, gate=None, norm="layer", e
     return out if y is None else (out, x_out)
 
 
+def _done(fn, done, lib):
+    """What the compiled marshalling returned: outputs, or the library's status."""
+    if type(done) is int:
+        raise FluxError(fn, done, lib)
+    return done
+
+
 def _scales(name, t, shape, dev):
     """(address, strides of a group's scales [..., rows, groups]); any strides."""
     import torch
@@ -873,6 +900,10 @@ def quantize_fp8(x, rows=1, out=None, scale=None, stream=None):
     import torch
 
     lib = _lib or load()
+    if stream is None and lib is _compiled_lib:
+        done = _compiled.quantize_fp8(x, rows, out, scale)
+        if done is not None:
+            return _done("flux_quantize_fp8", done, lib)
     dev, handle = _stream_of(x, stream)
     e4m3, shape, dtype = torch.float8_e4m3fn, x.shape, x.dtype
     if len(shape) not in (2, 3):
@@ -919,6 +950,10 @@ def linear_fp8(x, x_scale, w, w_scale, bias=None, act=None, gate=None, residual=
     import torch
 
     lib = _lib or load()
+    if stream is None and lib is _compiled_lib:
+        done = _compiled.linear_fp8(x, x_scale, w, w_scale, bias, act, gate, residual, out, status)
+        if done is not None:
+            return _done("flux_linear_fp8", done, lib)
     dev, handle = _stream_of(x, stream)
     bf16, e4m3, shape = torch.bfloat16, torch.float8_e4m3fn, x.shape
     if len(shape) not in (2, 3):
@@ -996,6 +1031,10 @@ def cross_attention(q, k, v, lengths=None, mask=None, scale=None, out=None, stat
     import torch
 
     lib = _lib or load()
+    if stream is None and lib is _compiled_lib:
+        done = _compiled.cross_attention(q, k, v, lengths, mask, scale, out, status)
+        if done is not None:
+            return _done("flux_cross_attention", done, lib)
     dev, handle = _stream_of(q, stream)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"q and k must be [B, S, H, D], got {tuple(q.shape)}, {tuple(k.shape)}")
@@ -1057,6 +1096,8 @@ def _own_status(lib, dev):
         if rc != 0:
             raise FluxError("flux_status_word", rc, lib)
         _own_words[dev] = word.value
+        if lib is _compiled_lib:
+            _compiled.own_word(dev, word.value)
     return _own_words[dev]
 
 

@@ -1,6 +1,7 @@
 """Builds the CUDA library libflux_attn.so in-tree with nvcc for sm_103a.
 
 Usage: ``python -m diffusion_transformer_joint_gb300.build [--force] [--checked]``.
+The binding's compiled marshalling is built beside it (marshal.cpp, with g++).
 ``--checked`` builds libflux_attn_checked.so instead: the same library compiled
 with -DFLUX_DEBUG, whose attention kernel checks its shared-memory, TMEM, TMA
 and exchange-buffer accesses and reports a failed check in the status word
@@ -44,6 +45,44 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def marshal_path() -> str:
+    """Where the compiled marshalling (marshal.cpp) lies, for this torch."""
+    import torch
+
+    return os.path.join(BUILD_DIR, f"torch-{torch.__version__}", "_marshal.so")
+
+
+def build_marshal(force: bool = False) -> str:
+    """Compile marshal.cpp against this torch; returns its path."""
+    import sysconfig
+
+    import torch
+
+    src, out = os.path.join(PKG, "marshal.cpp"), marshal_path()
+    header = os.path.join(INCLUDE, "flux_attn.h")
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(
+            os.path.getmtime(src), os.path.getmtime(header)):
+        return out
+    os.makedirs(os.path.dirname(out), exist_ok=True)
+    top = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-isystem", os.path.join(top, "include"),
+           "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(cuda, "include"), "-I", INCLUDE, src, "-o", tmp,
+           "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", f"-Wl,-rpath,{os.path.join(top, 'lib')}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed on marshal.cpp")
+    os.replace(tmp, out)
+    return out
+
+
 def build(force: bool = False, out: str = LIB_PATH, defines=(), verbose: bool = False) -> str:
     """Compile every csrc/*.cu into one shared library; returns its path."""
     os.makedirs(os.path.dirname(out), exist_ok=True)
@@ -77,3 +116,4 @@ if __name__ == "__main__":
         print(build_checked(force="--force" in sys.argv))
     else:
         print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+        print(build_marshal(force="--force" in sys.argv))
