@@ -30,7 +30,8 @@
  * projection (Q, K, V and the SwiGLU-activated MLP input from one GEMM), the
  * producer of the attention's inputs; and the rest of a block's operators:
  * the linear layers with bias, activation, gate and residual in the epilogue,
- * and the modulated norm with the gated residual in front.
+ * and the modulated norm with the gated residual in front; the linear layers over
+ * 8-bit operands with their quantisation; and attention to another sequence.
  *
  * Conventions shared by every entry point:
  *   - Device pointers refer to memory on the CUDA device that is current on
@@ -44,8 +45,8 @@
  *   - Device-side failures (a bounded wait inside a kernel that ran out)
  *     never trap: the kernel records FLUX_ERR_DEVICE_TIMEOUT in a status word
  *     and returns. Entry points with a workspace keep the word at its start
- *     (read it with flux_query_status()); the tabled attention, the projection
- *     and the linear layer take a device int32 instead, the caller's or the
+ *     (read it with flux_query_status()); the tabled attention, the projection,
+ *     the linear layers and the cross-attention take a device int32 instead, the caller's or the
  *     library's own (flux_status_word()).
  */
 #ifndef FLUX_ATTN_H
