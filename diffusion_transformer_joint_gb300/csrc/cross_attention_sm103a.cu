@@ -210,6 +210,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_addr(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
+  // Rows of a Q tile that no copy reaches (groups that do not divide 128): what
+  // another kernel left there would have a say in when their warp rescales.
+  const int q_rows = p.n_s * p.G;
+  if (q_rows < kTile) {
+    const int chunks = (kTile - q_rows) * 8;
+    for (int u = tid; u < L::kQTiles * (kD / 64) * chunks; u += kThreads)
+      st_shared_v4(sbase + static_cast<uint32_t>(u / chunks) * kBlockBytes +
+                       static_cast<uint32_t>(q_rows * 128 + u % chunks * 16),
+                   make_uint4(0u, 0u, 0u, 0u));
+    fence_proxy_async_smem();
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();

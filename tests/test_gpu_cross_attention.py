@@ -147,3 +147,17 @@ def test_nan_in_a_query_stays_in_its_row():
     want, bound = X.cross(**ops)
     want[0, 17, 1] = 0
     R.check(got, (want, bound + 2.0 ** -133), "the other rows")
+
+
+@pytest.mark.parametrize("Sq,D", [(42, 128), (42, 64), (3000, 128), (3000, 64)])
+def test_what_an_earlier_call_left_does_not_show(Sq, D):
+    """Groups of three fill 126 of a tile's 128 rows: whatever the call before had
+    in the other two, the bits are the same."""
+    ops = _make(2, Sq, 1000, 6, 2, D)
+    before = _make(1, 40000, 300, 1, 1, D, spread=300.0)  # every SM's query tiles
+    _run(before)
+    a = _run(ops)
+    before["q"].zero_()
+    _run(before)
+    b = _run(ops)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
