@@ -36,7 +36,8 @@
 // written as packed bf16 over the first 64 columns of S_t.
 //
 // The launch overlaps its prologue with the end of the kernel before it. Every
-// wait is bounded; one that runs out aborts the CTA and sets the status word to
+// wait is bounded (one for a whole item's work from the last tile on); one that
+// runs out aborts the CTA and sets the status word to
 // FLUX_ERR_DEVICE_TIMEOUT.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -83,7 +84,8 @@ struct Layout {
   static constexpr int kNumBars = kDrain + 1;
   static constexpr uint32_t kOffTmemSlot = kOffBar + 8 * kNumBars;
   static constexpr uint32_t kOffAbort = kOffTmemSlot + 4;
-  static constexpr uint32_t kSmemBytes = kOffAbort + 4;
+  static constexpr uint32_t kOffProgress = kOffAbort + 4;
+  static constexpr uint32_t kSmemBytes = kOffProgress + 4;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   // the parts of a narrow item: fp32 O of 128 rows over the drained K and V
   static constexpr uint32_t kPitch = kD * 4 + 16;
@@ -115,6 +117,27 @@ struct Item {
 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+// A wait for what takes a whole item's time, or several items': keys are not
+// limited, so that its budget begins anew whenever the producer of V has gone on.
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                          volatile const uint32_t *progress) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    uint32_t seen = *progress;
+    long long t0 = clock64();
+    while (!(ok = mbar_try_wait(bar, parity)) && !*abort_flag) {
+      const uint32_t now = *progress;
+      if (now != seen) {
+        seen = now;
+        t0 = clock64();
+      } else if (clock64() - t0 > kWaitBudgetCycles) {
+        *abort_flag = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
   __syncwarp();
@@ -172,6 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sbase + L::kOffBar + 8u * static_cast<uint32_t>(i); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + L::kOffTmemSlot);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(base + L::kOffAbort);
+  // tiles of V asked for so far
+  volatile uint32_t *progress = reinterpret_cast<volatile uint32_t *>(base + L::kOffProgress);
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5;
   const int lane = tid & 31;
@@ -204,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(L::kDrain), 1);
     *abort_flag = 0;
+    *progress = 0;
     fence_mbar_init();
   }
   if (warp == 2) {
@@ -331,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&maps.v);
       int s = 0;
       uint32_t turn = 0;
+      uint32_t asked = 0;                  // tiles so far
       uint32_t raw_par = 0, last_raw = 0;  // bit s: V-raw's next parity; the last copy's barrier
       bool ok = true;
       for (int i = first; ok && i < p.n_items; i += step) {
@@ -346,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kD / 64; ++c)
             tma_load_4d(dst + c * kBlockBytes, &maps.v, landed, c * 64, it.h, (it.lo + j) * kTile,
                         it.b);
+          *progress = ++asked;
           if (++s == kStages) s = 0, ++turn;
         }
       }
@@ -370,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!v_raw(it, j)) continue;
           uint32_t bits[4];
           key_bits(it, j, bits);
-          if (!(ok = wait_warp(bar(L::kVRaw + s), (raw_par >> s) & 1u, abort_flag))) break;
+          if (!(ok = wait_long(bar(L::kVRaw + s), (raw_par >> s) & 1u, abort_flag, progress))) break;
           raw_par ^= 1u << s;
           // the V rows that take no part, one per lane, its chunks in an order that
           // keeps eight lanes in different banks
@@ -726,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 st_global_v4(row_to() + q * 8, make_uint4(0u, 0u, 0u, 0u));
             continue;
           }
-          if (!(ok = wait_warp(bar(L::kRowFull + t), k & 1u, abort_flag))) break;
+          if (!(ok = wait_long(bar(L::kRowFull + t), k & 1u, abort_flag, progress))) break;
           const float l = ld_shared_f32(row_at(t, 1, row));
           const float inv_l = l == 0.f ? 0.f : 1.f / l;
           warp_arrive(bar(L::kRowFree + t), lane);
@@ -783,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m[2] = {kLowest, kLowest}, l[2] = {0.f, 0.f};
         for (int t = 0; t < 2; ++t) {
           if (it.n == 0) break;
-          if (!(ok = wait_warp(bar(L::kRowFull + t), k & 1u, abort_flag))) break;
+          if (!(ok = wait_long(bar(L::kRowFull + t), k & 1u, abort_flag, progress))) break;
           m[t] = ld_shared_f32(row_at(t, 0, row));
           l[t] = ld_shared_f32(row_at(t, 1, row));
           warp_arrive(bar(L::kRowFree + t), lane);

@@ -117,3 +117,43 @@ def test_cross_attention(withheld, B, Sq, Sk, H, lengths):
     _check(withheld, "flux_cross_attention",
            lambda status: binding.cross_attention(q, k, v, status=status, **kw),
            X.cross(q[:, rows], k, v, **kw), rows)
+
+
+@pytest.fixture(scope="module")
+def impatient(tmp_path_factory):
+    """A copy of the library whose waits are given 150 000 cycles (75 us)."""
+    regular = binding.load()
+    tmp = tmp_path_factory.mktemp("impatient")
+    src = tmp / "csrc"
+    shutil.copytree(build.CSRC, src)
+    text = (src / "ptx_sm103a.cuh").read_text()
+    assert text.count("kWaitBudgetCycles = 2000000000LL") == 1
+    (src / "ptx_sm103a.cuh").write_text(
+        text.replace("kWaitBudgetCycles = 2000000000LL", "kWaitBudgetCycles = 150000LL"))
+    out = tmp / "libflux_impatient.so"
+    flags = [x for x in build.NVCC_FLAGS if x not in ("-Xptxas", "-v")]
+    subprocess.run([build.nvcc(), *flags, "-I", build.INCLUDE, "-I", str(src),
+                    *sorted(str(p) for p in src.glob("*.cu")), "-o", str(out)],
+                   check=True, capture_output=True)
+    lib = ctypes.CDLL(str(out))
+    lib.flux_cross_attention.argtypes = regular.flux_cross_attention.argtypes
+    lib.flux_cross_attention.restype = ctypes.c_int
+    return lib
+
+
+@pytest.mark.parametrize("B,Sq,Sk,lengths", [
+    (1, 256, 131072, None),           # an item of a millisecond
+    (2, 38912, 32768, (32768, 300)),  # tiles with left-out keys after many items without
+    (1, 2, 524288, None),             # a cluster's parts
+    (1, 2, 524288, (524200,))])
+def test_long_items_are_no_timeout(impatient, B, Sq, Sk, lengths):
+    g = torch.Generator().manual_seed(81)
+    q, k, v = (torch.randn(B, n, 1, 128, generator=g).bfloat16().cuda() for n in (Sq, Sk, Sk))
+    kw = {} if lengths is None else dict(lengths=torch.tensor(lengths, dtype=torch.int32).cuda())
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with _With(impatient, "flux_cross_attention"):
+        got = binding.cross_attention(q, k, v, status=status, **kw)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    rows = torch.tensor([0, Sq - 1], device="cuda")
+    R.check(got[:, rows], X.cross(q[:, rows], k, v, **kw), "long")
