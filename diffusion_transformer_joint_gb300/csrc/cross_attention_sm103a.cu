@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                : it.keys - (it.lo + j) * kTile >= kTile;
         // Few queries' masks leave out some keys of every tile, say: their code stays
         // at hand, and replacing scores in registers is the faster way (one query over
-        // 12800 masked keys 19.3 us, 23.1 with the short loops below).
+        // 12800 masked keys 19.3 us in clusters of eight, 23.1 with the short loops below).
         constexpr bool kInPlace = kNarrow && kKeys == kMask;
         if (whole || kInPlace) {
           uint32_t sr[kTile];
@@ -1023,7 +1023,6 @@ cudaError_t launch(const CrossAttention &a, const CrossPlan &plan, int sms, int 
 
 }  // namespace
 
-constexpr int kFill16 = 112;
 CrossPlan plan_cross(const CrossAttention &a, int sms) {
   const int64_t n_s = kTile / (a.H / a.Hk), bh = a.B * a.Hk;
   const int64_t tiles = (a.Sk + kTile - 1) / kTile;
@@ -1031,14 +1030,20 @@ CrossPlan plan_cross(const CrossAttention &a, int sms) {
   const int64_t narrow = bh * ((a.Sq + n_s - 1) / n_s);
   auto waves = [&](int64_t n, int64_t slots) { return static_cast<double>((n + slots - 1) / slots); };
   CrossPlan best{false, 1, 2500.0 + waves(wide, sms) * (1100.0 * tiles + 1000.0)};
-  for (int parts = 1; parts <= kMaxParts && parts <= tiles; parts *= 2) {
-    // clusters of four and more do not fill every SM
-    const int64_t slots = parts == 16 ? sms * kFill16 / 152 / 16
-                          : parts == 8 ? sms * 120 / 152 / 8
-                          : parts == 4 ? sms * 144 / 152 / 4
-                                       : sms / parts;
+  // CTAs of clusters that fit 152 SMs at once: four and more do not fill every SM.
+  // (Eight key heads' 12800 keys, one query: 17.2 us in clusters of twelve, 19.3 of
+  // eight, 29.9 of sixteen, for which the eighth has to wait.)
+  struct Split {
+    int parts, ctas;
+    double join;
+  };
+  static constexpr Split kSplits[] = {{1, 152, 0.0},     {2, 152, 4500.0},  {4, 144, 4500.0},
+                                      {8, 120, 4500.0}, {12, 96, 4900.0}, {kMaxParts, 112, 5300.0}};
+  for (const auto &[parts, ctas, join] : kSplits) {
+    if (parts > tiles) break;
+    const int64_t slots = sms * ctas / 152 / parts;
     const double own = std::ceil(static_cast<double>(tiles) / parts);
-    const double per = 600.0 * own + 1400.0 + (parts > 1 ? 4500.0 : 0.0);
+    const double per = 600.0 * own + 1400.0 + join;
     const double ns = 2500.0 + waves(narrow, std::max<int64_t>(1, slots)) * per;
     if (ns < best.ns) best = CrossPlan{true, parts, ns};
   }

@@ -29,6 +29,7 @@ CROSS = {
     ("narrow", 2): (2, 73, 1950, 32, 32, 64),
     ("narrow", 4): (1, 5, 1750, 16, 16, 128),
     ("narrow", 8): (1, 39, 1155, 16, 8, 128),
+    ("narrow", 12): (1, 7, 6000, 24, 8, 128),
     ("narrow", 16): (1, 2, 5000, 8, 2, 64),
     ("wide", 1): (1, 3000, 300, 16, 8, 128),
 }
