@@ -162,6 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t bufs = tn == 64 ? 8 : tn == 128 ? 4 : 2;
   constexpr int feats = kGlu ? hw : tn;      // output features per tile
   constexpr int hfeats = feats / 2;          // of a half
+  // 16-column pieces that the sums' warps load at once (with two, the tile of 192
+  // columns spills)
+  constexpr int kStep = kPieces == 3 ? 1 : 2;
   constexpr uint32_t half_bytes = static_cast<uint32_t>(hw / 2) * kGroupK;  // W rows of this CTA
   constexpr uint32_t stage_bytes = kABytes + 2 * half_bytes;
 
@@ -434,14 +437,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sa = xs * __uint_as_float(ws.x), sb = xs * __uint_as_float(ws.y);
         tc_fence_after_sync();
         const uint32_t from = tmem + a * hw + lane_off;
-        // a piece at a time through the same registers: the FMAs are the bound (290
-        // cycles a group for the two warps of a scheduler), the loads take 6 more
-        // each; two pieces' registers in turn took half as long again
-        uint64_t v[8];
+        // kStep pieces at a time through the same registers: the FMAs take 290 cycles
+        // a group for the two warps of a scheduler, a load some more. (One piece at a
+        // time: 12288 -> 4096 channels of 4096 tokens 187.9 us, two 185.4; two whose
+        // registers take turns: half as long again.)
+        uint64_t v[8], v1[8];
 #pragma unroll
-        for (int k = 0; k < 2 * kPieces; ++k) {
-          tmem_ld16_pairs(from + k * 16, v);
-          if (k == 2 * kPieces - 1) {
+        for (int k = 0; k < 2 * kPieces; k += kStep) {
+          if constexpr (kStep == 2)
+            tmem_ld16_pairs2(from + k * 16, from + k * 16 + 16, v, v1);
+          else
+            tmem_ld16_pairs(from + k * 16, v);
+          if (k == 2 * kPieces - kStep) {
             // this warp's TMEM reads are complete: the columns may be reused
             tc_fence_before_sync();
             __syncwarp();
@@ -450,8 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ready = mbar_test_wait(
                 bar(kBarAccFull + static_cast<int>(2 * ((n + 1) % bufs)) + h), (n + 1) / bufs & 1u);
           }
-          add_scaled(acc + k * 8, v,
-                     (kGlu ? k < kPieces : kPieces != 3 || k < 2 * in_first) ? sa : sb);
+          // (both pieces lie in one block of W)
+          const float s = (kGlu ? k < kPieces : kPieces != 3 || k < 2 * in_first) ? sa : sb;
+          add_scaled(acc + k * 8, v, s);
+          if constexpr (kStep == 2) add_scaled(acc + (k + 1) * 8, v1, s);
         }
         if (in_slot == kScaleBatch - 1 || g == p.nk - 1) {
           __syncwarp();

@@ -643,6 +643,31 @@ __device__ __forceinline__ void tmem_ld16_pairs(uint32_t taddr, uint64_t (&r)[8]
       : "memory");
 }
 
+// Two such pieces, waited for once.
+__device__ __forceinline__ void tmem_ld16_pairs2(uint32_t taddr0, uint32_t taddr1, uint64_t (&r)[8],
+                                                 uint64_t (&s)[8]) {
+  asm volatile(
+      "{\n\t.reg .b32 t<16>, u<16>;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{u0,u1,u2,u3,u4,u5,u6,u7,u8,u9,u10,u11,u12,u13,u14,u15}, [%17];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "mov.b64 %0, {t0, t1};\n\tmov.b64 %1, {t2, t3};\n\t"
+      "mov.b64 %2, {t4, t5};\n\tmov.b64 %3, {t6, t7};\n\t"
+      "mov.b64 %4, {t8, t9};\n\tmov.b64 %5, {t10, t11};\n\t"
+      "mov.b64 %6, {t12, t13};\n\tmov.b64 %7, {t14, t15};\n\t"
+      "mov.b64 %8, {u0, u1};\n\tmov.b64 %9, {u2, u3};\n\t"
+      "mov.b64 %10, {u4, u5};\n\tmov.b64 %11, {u6, u7};\n\t"
+      "mov.b64 %12, {u8, u9};\n\tmov.b64 %13, {u10, u11};\n\t"
+      "mov.b64 %14, {u12, u13};\n\tmov.b64 %15, {u14, u15};\n\t}"
+      : "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3]), "=l"(r[4]), "=l"(r[5]), "=l"(r[6]),
+        "=l"(r[7]), "=l"(s[0]), "=l"(s[1]), "=l"(s[2]), "=l"(s[3]), "=l"(s[4]), "=l"(s[5]),
+        "=l"(s[6]), "=l"(s[7])
+      : "r"(taddr0), "r"(taddr1)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
