@@ -27,6 +27,11 @@
 // wait costs the sums' warps some 100 cycles). Warps 4-11 sums: one TMEM lane (a row of W) per
 // thread, 16 tokens at a time, the two warps of a lane quadrant taking turns.
 // Then all of them finish. Every wait is bounded, as in linear_split.
+//
+// Measured (GB300, in a graph): one token 4096 -> 4096 7.0 us (start 1, the bytes 2.6
+// at 6.4 TB/s, sums exchanged and finished 1.3, the rest the launch before), 96
+// tokens 9.2, 96 tokens 12288 -> 4096 14.7 (3.4 TB/s of W: a group of 96 tokens
+// takes an SM 0.28 us, its 28 KB come in 0.26).
 #include <algorithm>
 #include <cmath>
 #include <mutex>

