@@ -161,3 +161,29 @@ def test_what_an_earlier_call_left_does_not_show(Sq, D):
     _run(before)
     b = _run(ops)
     assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("B,Sq,Sk,H,Hk,D", [
+    (1, 7, 300, 100, 1, 64),      # a query's heads fill 100 of a tile's rows
+    (2, 300, 200, 66, 2, 128),    # groups of 33, three queries a tile
+    (1, 3, 4000, 127, 1, 128),    # keys over several CTAs
+    (1, 900, 129, 65, 1, 64)])
+def test_groups_that_do_not_fill_a_tile(B, Sq, Sk, H, Hk, D):
+    ops = _make(B, Sq, Sk, H, Hk, D, seed=H)
+    R.check(_run(ops), X.cross(**ops), f"{H} over {Hk}")
+
+
+@pytest.mark.parametrize("B,Sq,Sk,H,Hk,D", [(2, 1, 4000, 8, 2, 128), (3, 40, 100, 4, 4, 64),
+                                            (2, 3000, 300, 8, 8, 128), (1, 2000, 700, 3, 1, 64)])
+@pytest.mark.parametrize("kind", ["lengths", "mask", "both"])
+def test_no_key_for_anybody(B, Sq, Sk, H, Hk, D, kind):
+    ops = _make(B, Sq, Sk, H, Hk, D)
+    for name in ("k", "v"):
+        ops[name].fill_(float("nan"))
+    kw = {}
+    if kind != "mask":
+        kw["lengths"] = torch.zeros(B, dtype=torch.int32, device="cuda")
+    if kind != "lengths":
+        kw["mask"] = torch.zeros(B, Sk, dtype=torch.bool, device="cuda")
+    out = torch.full((B, Sq, H, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    assert bool((_run(ops, out=out, **kw) == 0).all())
