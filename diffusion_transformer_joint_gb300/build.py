@@ -10,6 +10,7 @@ and exchange-buffer accesses and reports a failed check in the status word
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import subprocess
 import sys
@@ -46,10 +47,20 @@ def nvcc() -> str:
 
 
 def marshal_path() -> str:
-    """Where the compiled marshalling (marshal.cpp) lies, for this torch."""
+    """Where the compiled marshalling lies, built for this torch from these sources:
+    a changed prototype asks for another file, never an older one's calls."""
     import torch
 
-    return os.path.join(BUILD_DIR, f"torch-{torch.__version__}", "_marshal.so")
+    digest = hashlib.sha256()
+    for p in _marshal_inputs():
+        with open(p, "rb") as f:
+            digest.update(f.read())
+    return os.path.join(BUILD_DIR, f"torch-{torch.__version__}",
+                        f"_marshal-{digest.hexdigest()[:16]}.so")
+
+
+def _marshal_inputs():
+    return [os.path.join(PKG, "marshal.cpp"), os.path.join(INCLUDE, "flux_attn.h")]
 
 
 def build_marshal(force: bool = False) -> str:
@@ -58,10 +69,8 @@ def build_marshal(force: bool = False) -> str:
 
     import torch
 
-    src, out = os.path.join(PKG, "marshal.cpp"), marshal_path()
-    header = os.path.join(INCLUDE, "flux_attn.h")
-    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(
-            os.path.getmtime(src), os.path.getmtime(header)):
+    src, out = _marshal_inputs()[0], marshal_path()
+    if not force and os.path.exists(out):
         return out
     os.makedirs(os.path.dirname(out), exist_ok=True)
     top = os.path.dirname(torch.__file__)
