@@ -14,6 +14,7 @@ import hashlib
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -47,8 +48,9 @@ def nvcc() -> str:
 
 
 def marshal_path() -> str:
-    """Where the compiled marshalling lies, built for this torch from these sources:
-    a changed prototype asks for another file, never an older one's calls."""
+    """Where the compiled marshalling lies, built for this torch and this Python from
+    these sources: a changed prototype asks for another file, never an older one's
+    calls."""
     import torch
 
     digest = hashlib.sha256()
@@ -56,7 +58,8 @@ def marshal_path() -> str:
         with open(p, "rb") as f:
             digest.update(f.read())
     return os.path.join(BUILD_DIR, f"torch-{torch.__version__}",
-                        f"_marshal-{digest.hexdigest()[:16]}.so")
+                        f"_marshal-{digest.hexdigest()[:16]}"
+                        + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
 def _marshal_inputs():
@@ -65,8 +68,6 @@ def _marshal_inputs():
 
 def build_marshal(force: bool = False) -> str:
     """Compile marshal.cpp against this torch; returns its path."""
-    import sysconfig
-
     import torch
 
     src, out = _marshal_inputs()[0], marshal_path()

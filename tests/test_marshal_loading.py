@@ -2,6 +2,7 @@
 from these sources."""
 import os
 import shutil
+import sysconfig
 
 from diffusion_transformer_joint_gb300 import build
 
@@ -23,3 +24,14 @@ def test_a_module_of_other_sources_has_another_name(tmp_path, monkeypatch):
         assert build.marshal_path() != before
         assert os.path.dirname(build.marshal_path()) == os.path.dirname(before)
         changed.write_text(text)
+
+
+def test_a_module_of_another_interpreter_has_another_name(monkeypatch):
+    """Two interpreters with the same torch in one tree: extension modules are not
+    theirs to share, and the name's ending says whose one is."""
+    before = build.marshal_path()
+    assert before.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    get = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var",
+                        lambda n: ".cpython-399.so" if n == "EXT_SUFFIX" else get(n))
+    assert build.marshal_path() != before and build.marshal_path().endswith(".cpython-399.so")
