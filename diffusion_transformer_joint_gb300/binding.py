@@ -51,16 +51,27 @@ _compiled_lib = None
 
 def _load_compiled(lib):
     """The compiled marshalling (build.build_marshal) of the calls that have one, over
-    `lib`; without it they are marshalled here."""
+    `lib`; without it, or without torch, they are marshalled here. A file that does not
+    load is warned of and passed over."""
     global _compiled, _compiled_lib
-    path = _build.marshal_path()
-    if not os.path.exists(path):
-        return
     import importlib.util
 
-    spec = importlib.util.spec_from_file_location("_marshal", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        path = _build.marshal_path()
+    except (ImportError, OSError):  # no torch, or no sources to tell the file by
+        return
+    if not os.path.exists(path):
+        return
+    try:
+        spec = importlib.util.spec_from_file_location("_marshal", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        import warnings
+
+        warnings.warn(f"the compiled marshalling does not load ({e}): calls are marshalled in "
+                      "Python", RuntimeWarning)
+        return
     module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in
                   ("flux_quantize_fp8", "flux_linear_fp8", "flux_cross_attention")))
     _compiled, _compiled_lib = module, lib

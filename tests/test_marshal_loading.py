@@ -1,10 +1,14 @@
 """Which file binding.load() takes as the compiled marshalling, on the CPU: one built
-from these sources."""
+from these sources, and none that does not load."""
 import os
 import shutil
+import subprocess
+import sys
 import sysconfig
 
-from diffusion_transformer_joint_gb300 import build
+import pytest
+
+from diffusion_transformer_joint_gb300 import binding, build
 
 
 def test_a_module_of_other_sources_has_another_name(tmp_path, monkeypatch):
@@ -35,3 +39,41 @@ def test_a_module_of_another_interpreter_has_another_name(monkeypatch):
     monkeypatch.setattr(sysconfig, "get_config_var",
                         lambda n: ".cpython-399.so" if n == "EXT_SUFFIX" else get(n))
     assert build.marshal_path() != before and build.marshal_path().endswith(".cpython-399.so")
+
+_LOAD = """
+import sys, warnings
+warnings.simplefilter("ignore")
+from diffusion_transformer_joint_gb300 import binding, build
+{}
+lib = binding.load()
+assert binding._compiled is None and binding._compiled_lib is None
+assert lib.flux_status_string(0)
+print("loaded")
+"""
+
+
+@pytest.mark.parametrize("spoil", [
+    "open(sys.argv[1], 'w').write('no module'); build.marshal_path = lambda: sys.argv[1]",
+    "open(sys.argv[1], 'w').close(); build.marshal_path = lambda: sys.argv[1]",
+    "build.marshal_path = lambda: build.LIB_PATH",   # a library, but no module
+    "sys.modules['torch'] = None",                   # no torch: the C functions alone
+    "build.INCLUDE = sys.argv[1]",                   # no header beside the package
+], ids=["text", "empty", "no-module", "no-torch", "no-header"])
+def test_without_a_module_that_loads_the_library_is_there(spoil, tmp_path):
+    """In a process of its own: load() returns the library, whose calls are marshalled
+    in Python."""
+    build.build()
+    r = subprocess.run([sys.executable, "-c", _LOAD.format(spoil), str(tmp_path / "_marshal.so")],
+                       capture_output=True, text=True, cwd=build.ROOT)
+    assert r.stdout == "loaded\n", r.stderr
+
+
+def test_a_module_that_does_not_load_is_said(tmp_path, monkeypatch):
+    bad = tmp_path / "_marshal.so"
+    bad.write_text("no module")
+    monkeypatch.setattr(build, "marshal_path", lambda: str(bad))
+    monkeypatch.setattr(binding, "_compiled", None)
+    monkeypatch.setattr(binding, "_compiled_lib", None)
+    with pytest.warns(RuntimeWarning, match="marshalled in Python"):
+        binding._load_compiled(object())
+    assert binding._compiled is None
