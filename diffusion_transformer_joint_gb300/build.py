@@ -1,7 +1,8 @@
 """Builds the CUDA library libflux_attn.so in-tree with nvcc for sm_103a.
 
 Usage: ``python -m diffusion_transformer_joint_gb300.build [--force] [--checked]``.
-The binding's compiled marshalling is built beside it (marshal.cpp, with g++).
+The binding's compiled marshalling is built beside it (marshal.cpp, with g++ and
+torch's headers) where those are there; without it calls are marshalled in Python.
 ``--checked`` builds libflux_attn_checked.so instead: the same library compiled
 with -DFLUX_DEBUG, whose attention kernel checks its shared-memory, TMEM, TMA
 and exchange-buffer accesses and reports a failed check in the status word
@@ -121,9 +122,26 @@ def build_checked(force: bool = False, out: str = CHECKED_LIB_PATH) -> str:
     return build(force=force, out=out, defines=("FLUX_DEBUG",))
 
 
-if __name__ == "__main__":
+def try_build_marshal(force: bool = False):
+    """build_marshal(), or None and a message where g++ or torch's headers are missing:
+    the binding then marshals every call in Python."""
+    try:
+        return build_marshal(force)
+    except (ImportError, OSError, RuntimeError) as e:
+        sys.stderr.write(f"compiled marshalling not built ({e}): calls are marshalled in Python\n")
+        return None
+
+
+def main() -> int:
     if "--checked" in sys.argv:
         print(build_checked(force="--force" in sys.argv))
-    else:
-        print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
-        print(build_marshal(force="--force" in sys.argv))
+        return 0
+    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    path = try_build_marshal(force="--force" in sys.argv)
+    if path is not None:
+        print(path)
+    return 0
+
+
+if __name__ == "__main__":
+    sys.exit(main())

@@ -8,6 +8,7 @@ import sysconfig
 
 import pytest
 
+import __graft_entry__
 from diffusion_transformer_joint_gb300 import binding, build
 
 
@@ -77,3 +78,20 @@ def test_a_module_that_does_not_load_is_said(tmp_path, monkeypatch):
     with pytest.warns(RuntimeWarning, match="marshalled in Python"):
         binding._load_compiled(object())
     assert binding._compiled is None
+
+
+@pytest.mark.parametrize("fault", [FileNotFoundError("g++"), RuntimeError("g++ failed"),
+                                   ModuleNotFoundError("torch")], ids=lambda e: type(e).__name__)
+def test_the_build_goes_on_without_the_marshalling(fault, monkeypatch, capsys):
+    """Without g++ or torch's headers the library and the oracle are built all the
+    same, and the message says what is missing."""
+    def fail(force=False):
+        raise fault
+
+    monkeypatch.setattr(build, "build_marshal", fail)
+    __graft_entry__.build()
+    assert str(fault) in capsys.readouterr().err
+    monkeypatch.setattr(sys, "argv", ["build.py"])
+    assert build.main() == 0
+    said = capsys.readouterr()
+    assert said.out.strip() == build.LIB_PATH and str(fault) in said.err
