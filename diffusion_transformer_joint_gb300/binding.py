@@ -1027,6 +1027,17 @@ def _head_rows(name, t, shape, dev):
     return t.data_ptr(), bs, rs
 
 
+def _softmax_scale(scale):
+    """The scale as the library takes it: 0 for its default. What fp32 rounds to 0, which
+    would stand for that, is refused, as is what times log2(e) is no longer finite."""
+    if scale is None:
+        return 0.0
+    value = ctypes.c_float(float(scale)).value
+    if not 0.0 < value <= 2.0 ** 127:
+        raise ValueError(f"scale must be positive in fp32 and at most 2^127, got {scale}")
+    return value
+
+
 def cross_attention(q, k, v, lengths=None, mask=None, scale=None, out=None, status=None,
                     stream=None):
     """Attention to another sequence: softmax(scale q k^T) v over the keys that take part.
@@ -1036,8 +1047,8 @@ def cross_attention(q, k, v, lengths=None, mask=None, scale=None, out=None, stat
     between tokens and batch elements (two halves of one product's output).
     lengths: int32 [B], keys from there on take no part; mask: bool or uint8 [B,
     Sk], nor do keys where it is 0 (their k and v may hold anything). A row that
-    no key is left for is zero. scale: 1 / sqrt(D) unless given. ``out`` bf16 of
-    q's shape; ``status`` as for linear. Returns out.
+    no key is left for is zero. scale: 1 / sqrt(D) unless given; above 0 in fp32, at
+    most 2^127. ``out`` bf16 of q's shape; ``status`` as for linear. Returns out.
     """
     import torch
 
@@ -1070,15 +1081,12 @@ def cross_attention(q, k, v, lengths=None, mask=None, scale=None, out=None, stat
             raise ValueError(f"mask must be bool or uint8 [{B}, {Sk}] on cuda:{dev} with its keys "
                              f"adjacent, got {mask.dtype} {tuple(mask.shape)} on {mask.device}")
         mp, mb = mask.data_ptr(), mask.stride(0) if B > 1 else 0
-    if scale is None:
-        scale = 0.0
-    elif not 0.0 < scale < 3e38:
-        raise ValueError(f"scale must be finite and positive, got {scale}")
+    scale = _softmax_scale(scale)
     if out is None:
         out = _allocate(stream, torch.empty, shape, dtype=torch.bfloat16, device=q.device)
     op, ob, orow = _head_rows("out", out, shape, dev)
     rc = lib.flux_cross_attention(qp, qb, qr, kp, kb, kr, vp, vb, vr, lp, mp, mb, B, Sq, Sk, H, Hk,
-                                  D, float(scale), op, ob, orow, _status_pointer(lib, status, dev),
+                                  D, scale, op, ob, orow, _status_pointer(lib, status, dev),
                                   handle)
     if rc != 0:
         raise FluxError("flux_cross_attention", rc, lib)

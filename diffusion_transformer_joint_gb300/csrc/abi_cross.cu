@@ -20,7 +20,8 @@ extern "C" int flux_cross_attention(const void *q, int64_t q_bs, int64_t q_rs, c
   if (B < 1 || Sq < 1 || Sk < 1 || Sq > kMaxTokens / B || Sk > kMaxTokens / B || H < 1 || Hk < 1 ||
       H > 65536 || H % Hk != 0 || H / Hk > 128 || (D != 64 && D != 128))
     return FLUX_ERR_SHAPE;
-  if (!(scale >= 0.f) || !std::isfinite(scale)) return FLUX_ERR_SHAPE;
+  // times log2(e) it has to be finite (and is not where it is no number)
+  if (!(scale >= 0.f) || !(scale <= 0x1p127f)) return FLUX_ERR_SHAPE;
   // batch elements, key heads and blocks of at least 128 H / Hk rows: an item each
   const int64_t n_s = 128 / (H / Hk);
   if ((Sq + n_s - 1) / n_s > (int64_t{1} << 24) / Hk / B) return FLUX_ERR_SHAPE;

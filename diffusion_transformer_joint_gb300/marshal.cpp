@@ -256,11 +256,13 @@ PyObject *cross(PyObject *const *a) {
     mask = static_cast<const uint8_t *>(t->const_data_ptr());
     mask_bs = B > 1 ? t->stride(0) : 0;
   }
-  double scale = 0.0;
+  float scale = 0.f;  // (the library's default)
   if (!absent(a[5])) {
     if (!PyFloat_Check(a[5])) return nullptr;
-    scale = PyFloat_AS_DOUBLE(a[5]);
-    if (!(scale > 0.0 && scale < 3e38)) return nullptr;
+    const double given = PyFloat_AS_DOUBLE(a[5]);
+    if (!(given <= 0x1p127)) return nullptr;
+    scale = static_cast<float>(given);
+    if (!(scale > 0.f)) return nullptr;
   }
   int32_t *status;
   if (!take_status(a[7], dev, status)) return nullptr;
@@ -269,8 +271,8 @@ PyObject *cross(PyObject *const *a) {
   if (!take_heads(absent(a[6]) ? &out : tensor(a[6]), B, Sq, H, D, dev, ro)) return nullptr;
   const int rc = cross_fn(rq.p, rq.bs, rq.rs, rk.p, rk.bs, rk.rs, rv.p, rv.bs, rv.rs, lengths, mask,
                           mask_bs, static_cast<int>(B), Sq, Sk, static_cast<int>(H),
-                          static_cast<int>(Hk), static_cast<int>(D), static_cast<float>(scale), ro.p,
-                          ro.bs, ro.rs, status, stream);
+                          static_cast<int>(Hk), static_cast<int>(D), scale, ro.p, ro.bs,
+                          ro.rs, status, stream);
   return rc != FLUX_OK ? PyLong_FromLong(rc) : given_or(a[6], out);
 }
 

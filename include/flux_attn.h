@@ -556,7 +556,7 @@ int flux_linear_fp8(const void *x, int64_t x_bs, int64_t x_rs, const float *x_sc
  *              NULL (all 1). Any alignment.
  *   B, Sq, Sk  1 <= B * Sq, B * Sk <= 2^30; at most 2^24 blocks of 128 Hk / H
  *              queries (rounded down) per key head of all batch elements.
- *   scale      finite, > 0; 0 stands for 1 / sqrt(D).
+ *   scale      > 0 and at most 2^127; 0 stands for 1 / sqrt(D).
  *   out        bf16 [B, Sq, H, D].
  *   status     as for flux_linear.
  * The sums are added in an order that depends on the sizes only.
