@@ -11,7 +11,8 @@
 // Softmax in the log2 domain, one pass: per row a running maximum m and sum l in
 // fp32, p = 2^(s scale log2(e) - m) rounded to bf16 for the second product, O and
 // l rescaled only when m grows by more than 8 (a factor of 256), exact after the
-// final division by l. A key that does not take part has p = 0: its score is
+// final division by l (where |m| passes 2^24 the score's product is rounded like m's
+// before m is taken off: see kFar). A key that does not take part has p = 0: its score is
 // replaced before the maximum, and its row of V, which may hold anything, is
 // zeroed in shared memory, for 0 times infinity or NaN is NaN.
 //
@@ -62,6 +63,7 @@ constexpr int kTile = 128;  // rows of a query tile, keys of a key tile
 constexpr int kThreads = 512;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr float kLowest = -3.0e38f;        // a maximum no key has been counted in
+constexpr float kFar = 16777216.f;         // 2^24: maxima from here on are multiples of 2
 constexpr uint32_t kBlockBytes = 16384;    // 128 rows x 64 channels, one swizzle block
 constexpr uint32_t kBoxBytes = 32 * 128;   // epilogue: 32 rows x 64 channels
 constexpr uint32_t kTmemCols = 512;
@@ -144,6 +146,10 @@ __device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, volatil
     }
   }
   return __all_sync(0xffffffffu, ok);
+}
+// Whether a row's maximum is so far from 0 that its rounding shows in p.
+__device__ __forceinline__ bool is_far(float m) {
+  return fabsf(m) >= kFar && m != kLowest;
 }
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
   __syncwarp();
@@ -574,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = first; ok && i < p.n_items; i += step) {
       const Item it = item_at(i);
       float m_run = kLowest, l_run = 0.f;
-      bool fresh = true;
+      bool fresh = true, far = false;  // far: the maximum of a row of the warp is
       // a warp without rows of the tensor takes part in the hand-offs only (its P
       // is whatever was there, for rows that nobody reads)
       const int s_tile = it.s0 + (kNarrow ? 0 : t * p.n_s);
@@ -595,10 +601,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f, m_use = m_run;
         auto rise = [&](float mx) {
           mx = fmaxf(mx * scale_log2, kLowest);  // (no key so far: p is 2^-inf below)
+          const bool any = __any_sync(0xffffffffu, fresh ? is_far(mx) : mx > m_run + kRescaleThreshold);
           if (fresh) {
             m_use = mx;
-          } else if (__any_sync(0xffffffffu, mx > m_run + kRescaleThreshold)) {
+            far = any;
+          } else if (any) {
             m_use = fmaxf(m_run, mx);
+            far = __any_sync(0xffffffffu, is_far(m_use));
             alpha = ex2_approx(m_run - m_use);
             // S_t of this tile is complete, hence so is PV_t before it: O_t is stable
 #pragma unroll 1
@@ -626,10 +635,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return fmaxf(a, b);
         };
+        // Far from 0 the maximum's own rounding, half an ulp, is what the largest key's
+        // exponent comes out as (100 and more at 2^32, where p would overflow or vanish).
+        // There scores are scaled, and rounded, like the maximum before it is taken off:
+        // times pre here, times factor in weigh. For the warp's other rows pre is 1.
+        auto scale_first = [&](uint32_t *sc) {
+          const float pre = is_far(m_use) ? scale_log2 : 1.f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            sc[e] = __float_as_uint(__fmul_rn(__uint_as_float(sc[e]), pre));
+          return is_far(m_use) ? 1.f : scale_log2;
+        };
         // p of 32 scores, packed to bf16, and its sums
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-        auto weigh = [&](const uint32_t *sc, uint32_t (&pk)[16]) {
-          const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
+        auto weigh = [&](const uint32_t *sc, uint32_t (&pk)[16], float factor) {
+          const uint64_t scale2 = f2_pack(factor, factor);
           const uint64_t negm2 = f2_pack(-m_use, -m_use);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -661,11 +681,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = 0; w < 4; ++w) mr[w] = leave_out(&sr[w * 32], bits[w]);
           }
           rise(fmax3(mr[0], mr[1], fmaxf(mr[2], mr[3])));
+          if (!far) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
-            weigh(&sr[c * 32], pk);
-            tmem_st16(tS + c * 16, pk);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t pk[16];
+              weigh(&sr[c * 32], pk, scale_log2);
+              tmem_st16(tS + c * 16, pk);
+            }
+          } else {  // (rare: read once more, so that this needs no registers above)
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t sc[32], pk[16];
+              tmem_ld32(tS + c * 32, sc);
+              tmem_ld_wait();
+              if (kInPlace && !whole)
+                (void)leave_out(sc, c == 0 ? bits[0] : c == 1 ? bits[1] : c == 2 ? bits[2] : bits[3]);
+              const float factor = scale_first(sc);
+              weigh(sc, pk, factor);
+              tmem_st16(tS + c * 16, pk);
+            }
           }
         } else {
           // Some keys take no part: 32 keys at a time in short loops, for this code,
@@ -705,7 +739,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t sc[32];
               tmem_ld32(tS + c * 32, sc);
               tmem_ld_wait();
-              weigh(sc, pk);
+              const float factor = far ? scale_first(sc) : scale_log2;
+              weigh(sc, pk, factor);
             }
             tmem_st16(tS + c * 16, pk);
           }

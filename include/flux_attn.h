@@ -543,7 +543,8 @@ int flux_linear_fp8(const void *x, int64_t x_bs, int64_t x_rs, const float *x_sc
  * G = H / Hk, over the keys j that take part: j below lengths[b], and mask[b, j]
  * not 0. What k and v hold for the others is not looked at (it may be NaN). A
  * row that no key is left for is 0. Sums and the softmax are fp32, the weights
- * are rounded to bf16 for the product with v, and each output once to bf16.
+ * are rounded to bf16 for the product with v, and each output once to bf16. Scores
+ * may be as large as fp32 takes them: |q . k| and |scale q . k| below 2^127.
  *
  *   q          device, bf16 [B, Sq, H, D], D 64 or 128: a token's heads are
  *              adjacent; strides between tokens (_rs) and batch elements (_bs) as
