@@ -13,7 +13,10 @@ The compute runs in the CUDA library built from ``csrc/`` (C-ABI declared in
   projection, writing Q, K, V in the attention's [B, S, H, 128] layout;
 - ``linear``: a block's other products, with bias, activation, gate and
   residual in the epilogue;
-- ``modulated_norm``: the modulated norm with the gated residual in front.
+- ``modulated_norm``: the modulated norm with the gated residual in front;
+- ``quantize_fp8`` and ``linear_fp8``: ``linear`` over 8-bit operands with a scale
+  per 128 channels, and what makes them;
+- ``cross_attention``: attention to another sequence (an encoder's states).
 
 Importing this package does not load the library; the first call does, and
 fails loudly when it is missing (there is no CPU path).

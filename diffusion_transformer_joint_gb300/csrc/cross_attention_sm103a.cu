@@ -18,10 +18,11 @@
 //
 // Two forms, chosen by plan_cross (sizes alone):
 //   wide    (many queries) a CTA owns two tiles of queries and walks every key
-//           tile for both; persistent, items round robin. Keys are few here, so
-//           an item is short: Q tiles are loaded, multiplied and stored on their
-//           own, and the next item's first products are issued before this one's
-//           last values are read, without a break at its end.
+//           tile for both; persistent, items round robin. Where keys are few (a
+//           prompt's one to four tiles) items are short: so Q tiles are loaded,
+//           multiplied and stored on their own, and the next item's first products
+//           are issued before this one's last values are read, without a break at
+//           its end.
 //   narrow  (few queries) a CTA owns one tile of queries and a range of the keys,
 //           whose tiles go in turn to two streams with a softmax and an O each;
 //           C CTAs of a cluster split the keys. The parts are joined through
@@ -41,11 +42,15 @@
 // runs out aborts the CTA and sets the status word to
 // FLUX_ERR_DEVICE_TIMEOUT.
 //
-// Measured (GB300, in a graph): 12800 queries x 4096 keys, 48 heads 740 to 750 us
-// (1730 TFLOP/s); 2 x 4056 queries over prompts padded to 512, 32 heads, lengths 53 to
-// 57 (an item's chain S, softmax of 0.6 us, PV; tensor cores 45% active); 64 queries
-// over 2 x 4096 keys, 32 heads 27.5 (4.9 TB/s); one query over 12800 masked keys, 32
-// heads over 8 17.2 (3.1 TB/s: 96 CTAs, and what an SM takes in).
+// Measured (GB300, in a graph of 2 ms; heads of 128 channels, and of 64): 12800 queries
+// x 4096 keys, 48 heads 751 to 765 us (1700 TFLOP/s; 825 in calls for a second, at the
+// power limit), 684; 2 x 4056 queries over prompts padded to 512, 32 heads, with lengths
+// 50 to 52 (an item's chain S, softmax of 0.6 us, PV; tensor cores 45% active), 42, with a
+// mask for the same padding 67, 56; 12800 over 512, 32 heads 81, 71, with a random mask
+// 118, 112; 64 queries over 2 x 4096 keys, 32 heads 27.8 (4.8 TB/s), 19.7; one query over
+// 12800 masked keys, 32 heads over 8 17.7 (3.0 TB/s: 96 CTAs, and what an SM takes in),
+// 14.8. -Xptxas -v reports spills of 24 to 36 bytes a thread in the wide form at 128
+// channels and 16 in the narrow one with a mask.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1072,8 +1077,9 @@ CrossPlan plan_cross(const CrossAttention &a, int sms) {
   auto waves = [&](int64_t n, int64_t slots) { return static_cast<double>((n + slots - 1) / slots); };
   CrossPlan best{false, 1, 2500.0 + waves(wide, sms) * (1100.0 * tiles + 1000.0)};
   // CTAs of clusters that fit 152 SMs at once: four and more do not fill every SM.
-  // (Eight key heads' 12800 keys, one query: 17.2 us in clusters of twelve, 19.3 of
-  // eight, 29.9 of sixteen, for which the eighth has to wait.)
+  // (Eight key heads' 12800 keys, one query, the one size that the row of twelve was
+  // measured for: 17.2 us in clusters of twelve, 19.3 of eight, 29.9 of sixteen, for
+  // which the eighth has to wait.)
   struct Split {
     int parts, ctas;
     double join;

@@ -32,16 +32,18 @@
 // memory, the vectors of a tile and the bounded waits are as in linear_pair. The
 // epilogue takes its values from registers; the MMAs meanwhile run on for two
 // groups. A residual's boxes are fetched while the tile's groups are added: three
-// boxes a warp and five stages of ring with one, else two and six.
+// boxes a warp with one, else two. The ring has the rest of the shared memory: five
+// stages of 256 columns either way, 6, 7 and 8 (9 without a residual) of 192, 128 and 64.
 //
 // 12 warps per CTA: warp 0 TMA producer, warps 1 and 2 MMA issuers of a half each
 // (even CTA; one warp for both took longer to issue a group's MMAs, between waits
 // of some 100 cycles, than they run), warp 2 TMEM allocation, warps 4-7 and 8-11
 // the sums of the two halves.
 //
-// Measured (GB300, in a graph): 4096 tokens 4096 -> 4096 with gate and residual 78 us
-// (1766 TFLOP/s), 4056 tokens 4096 -> SwiGLU 12288 363 (2250), 12800 tokens 18432 ->
-// 6144 1100 (2640). A group takes 0.43 us at 256 columns (its MMAs 0.26, its copies
+// Measured (GB300, in a graph of 2 ms; in brackets calls for a second or more, at the
+// power limit): 4096 tokens 4096 -> 4096 with gate and residual 79 us, 1745 TFLOP/s
+// (79), 4056 tokens 4096 -> SwiGLU 12288 373, 2190 (381), 12800 tokens 18432 -> 6144
+// 1110, 2610 (1240, 2340). A group takes 0.43 us at 256 columns (its MMAs 0.26, its copies
 // 0.29): a half's columns go from MMAs to sums and back, and TMEM holds two of them.
 // At 64 and 128 columns it takes 0.28, and still 0.26 to 0.27 without its MMAs,
 // W's copies or its additions: a chain of hand-offs, none of which is alone the bound.
